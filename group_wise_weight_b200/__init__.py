@@ -110,6 +110,21 @@ def lib():
         L.wq_decode_attention_int4.restype = I
         L.wq_decode_attention_fp8.argtypes = [P, P, P, P, P, P, I64, I64, I64, I64, I64, P, P, SZ, P]
         L.wq_decode_attention_fp8.restype = I
+        L.wq_quantize_int8_tokens.argtypes = [P, I, I64, I64, I64, P, P, P]
+        L.wq_quantize_int8_tokens.restype = I
+        L.wq_gemm_w8a8_int8_workspace_bytes.argtypes = [I64, I64, I64]
+        L.wq_gemm_w8a8_int8_workspace_bytes.restype = SZ
+        L.wq_gemm_w8a8_int8.argtypes = [P, P, I64, I64, I64, P, P, P, P, SZ, P]
+        L.wq_gemm_w8a8_int8.restype = I
+        L.wq_qk_norm_rope.argtypes = [P, I64, P, I64, P, P, ctypes.c_float, P, P, I64, I, I64, I64, I64, I64, P, I64,
+                                      P, I64, P]
+        L.wq_qk_norm_rope.restype = I
+        L.wq_kv_store_int4.argtypes = [P, I64, P, I64, P, I64, I64, I64, I64, P, P, P, P, P, P, P]
+        L.wq_kv_store_int4.restype = I
+        L.wq_kv_store_fp8.argtypes = [P, I64, P, I64, P, I64, I64, I64, I64, P, P, P, P, P]
+        L.wq_kv_store_fp8.restype = I
+        L.wq_prompt_attention.argtypes = [P, I64, P, I64, P, I64, P, I64, I64, I64, I64, I64, P, I64, P]
+        L.wq_prompt_attention.restype = I
         _lib = L
     return _lib
 
@@ -534,3 +549,183 @@ def wq_awq_channel_scales(magnitudes: torch.Tensor, alpha: float, col_scale=None
     _check(lib().wq_awq_channel_scales(_dev(magnitudes, "magnitudes"), K, float(alpha), _dev(col_scale, "col_scale"),
                                        _stream_handle(stream)))
     return col_scale
+
+
+# ---- The prompt side: per-token INT8, W8A8 INT8 matmul, norms and positions, cache stores, prompt attention ----
+
+def _on(device, fn, stream, *args):
+    """Call fn(*args, stream) with `device` current, on its current stream unless one is given."""
+    if device.index == torch.cuda.current_device():
+        _check(fn(*args, _stream_handle(stream)))
+    else:
+        with torch.cuda.device(device):
+            _check(fn(*args, _stream_handle(stream)))
+
+
+def _dense_as(t: torch.Tensor, name: str, dtype, shape, device) -> int:
+    """Address of a contiguous tensor of this type and shape on this device."""
+    ptr = _dev(t, name)
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, not on {device}")
+    _dense(t, name)
+    return ptr
+
+
+def _heads_of(t: torch.Tensor, name: str, device=None, shape=None):
+    """(address, row distance) of a bf16 [tokens][heads][D] tensor whose rows hold their heads one after another."""
+    ptr = _dev(t, name)
+    if t.dtype != torch.bfloat16 or t.dim() != 3:
+        raise TypeError(f"{name} must be a 3-D bfloat16 tensor [tokens][heads][D]")
+    if device is not None and t.device != device:
+        raise ValueError(f"{name} is on {t.device}, not on {device}")
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
+    M, H, D = t.shape
+    if (D > 1 and t.stride(2) != 1) or (H > 1 and t.stride(1) != D):
+        raise ValueError(f"{name} must hold each token's heads one after another (strides D and 1)")
+    return ptr, (t.stride(0) if M > 1 else H * D)
+
+
+def wq_quantize_int8_tokens(x: torch.Tensor, q=None, scales=None, stream=None):
+    """Symmetric INT8 with one binary32 scale per row (token) of x: [M][K] (row stride >= K) fp32 or bf16 on CUDA.
+
+    Returns (q int8 [M][K], scales float32 [M]), the left operand of wq_gemm_w8a8_int8."""
+    px = _dev(x, "x")
+    if x.dim() != 2 or (x.stride(1) != 1 and x.shape[1] > 1):
+        raise ValueError("x must be a 2-D tensor with unit stride along K")
+    xtype = _wtype(x)
+    M, K = x.shape
+    q = torch.empty((M, K), dtype=torch.int8, device=x.device) if q is None else q
+    scales = torch.empty((M,), dtype=torch.float32, device=x.device) if scales is None else scales
+    _on(x.device, lib().wq_quantize_int8_tokens, stream, px, xtype, M, K, x.stride(0) if M > 1 else K,
+        _dense_as(q, "q", torch.int8, (M, K), x.device), _dense_as(scales, "scales", torch.float32, (M,), x.device))
+    return q, scales
+
+
+def wq_gemm_w8a8_int8_workspace_bytes(M: int, N: int, K: int) -> int:
+    return int(lib().wq_gemm_w8a8_int8_workspace_bytes(int(M), int(N), int(K)))
+
+
+def wq_gemm_w8a8_int8(xq: torch.Tensor, xscales: torch.Tensor, qweight: torch.Tensor, scales: torch.Tensor, y=None,
+                      workspace=None, stream=None) -> torch.Tensor:
+    """y[M][N] = (xq . qweight^T) * xscales[m] * scales[n], INT8 codes multiplied on the tensor cores with exact
+    integer sums.  xq int8 [M][K] and xscales float32 [M] from wq_quantize_int8_tokens, qweight int8 [N][K] and
+    scales bf16 ([N] or [N][1]) from wq_quantize_int8 with one scale per output channel.  bf16 out."""
+    pxq, dev = _dev(xq, "xq"), xq.device
+    if xq.dtype != torch.int8 or qweight.dtype != torch.int8 or xq.dim() != 2 or qweight.dim() != 2:
+        raise TypeError("xq and qweight must be 2-D int8 tensors")
+    _dense(xq, "xq")
+    M, K = xq.shape
+    N = qweight.shape[0]
+    y = torch.empty((M, N), dtype=torch.bfloat16, device=dev) if y is None else y
+    if workspace is None:
+        with torch.cuda.device(dev):
+            need = wq_gemm_w8a8_int8_workspace_bytes(M, N, K)
+        workspace = torch.zeros(need, dtype=torch.uint8, device=dev)
+    elif workspace.device != dev:
+        raise ValueError(f"workspace is on {workspace.device}, not on {dev}")
+    _dense(workspace, "workspace")
+    _on(dev, lib().wq_gemm_w8a8_int8, stream, pxq, _dense_as(xscales, "xscales", torch.float32, (M,), dev), M, N, K,
+        _dense_as(qweight, "qweight", torch.int8, (N, K), dev),
+        _dense_as(scales, "scales", torch.bfloat16, (N,) if scales.dim() == 1 else (N, 1), dev),
+        _dense_as(y, "y", torch.bfloat16, (M, N), dev), _dev(workspace, "workspace"),
+        workspace.numel() * workspace.element_size())
+    return y
+
+
+def wq_qk_norm_rope(q: torch.Tensor, k: torch.Tensor, positions: torch.Tensor, inv_freq: torch.Tensor, q_weight=None,
+                    k_weight=None, eps: float = 1e-6, interleaved: bool = False, q_out=None, k_out=None, stream=None):
+    """RMS norms of each query and key head (when both weights, bf16 [D], are given) and rotary positions, one pass.
+
+    q [M][Hq][D], k [M][H][D] bf16 on CUDA, heads adjacent, any row stride (slices of a fused projection);
+    positions int32 [M]; inv_freq float32 [rot / 2]: the first rot values of a head turn by position * inv_freq,
+    in pairs (i, i + rot / 2), or (2i, 2i + 1) when `interleaved`.  q_out and k_out may be q and k (in place).
+    Returns (q_out, k_out), dense bf16 unless given."""
+    dev = q.device
+    pq, ldq = _heads_of(q, "q")
+    M, Hq, D = q.shape
+    pk, ldk = _heads_of(k, "k", dev)
+    H = k.shape[1]
+    if k.shape[0] != M or k.shape[2] != D:
+        raise ValueError("q and k must have the same tokens and head size")
+    if inv_freq.dim() != 1:
+        raise ValueError("inv_freq must be a 1-D tensor")
+    q_out = torch.empty((M, Hq, D), dtype=torch.bfloat16, device=dev) if q_out is None else q_out
+    k_out = torch.empty((M, H, D), dtype=torch.bfloat16, device=dev) if k_out is None else k_out
+    pqo, ldqo = _heads_of(q_out, "q_out", dev, (M, Hq, D))
+    pko, ldko = _heads_of(k_out, "k_out", dev, (M, H, D))
+    half = inv_freq.numel()
+    _on(dev, lib().wq_qk_norm_rope, stream, pq, ldq, pk, ldk,
+        None if q_weight is None else _dense_as(q_weight, "q_weight", torch.bfloat16, (D,), dev),
+        None if k_weight is None else _dense_as(k_weight, "k_weight", torch.bfloat16, (D,), dev), float(eps),
+        _dense_as(positions, "positions", torch.int32, (M,), dev),
+        _dense_as(inv_freq, "inv_freq", torch.float32, (half,), dev), 2 * half, int(bool(interleaved)), M, Hq, H, D,
+        pqo, ldqo, pko, ldko)
+    return q_out, k_out
+
+
+def _store_rows(k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, k_codes: torch.Tensor):
+    dev = k.device
+    pk, ldk = _heads_of(k, "k")
+    pv, ldv = _heads_of(v, "v", dev, k.shape)
+    M, H, D = k.shape
+    if k_codes.dim() != 4 or k_codes.shape[2] != H:
+        raise ValueError("the codes must be [B][T][H][...] with k's heads")
+    ps = _dense_as(slots, "slots", torch.int64, (M,), dev)
+    return dev, (pk, ldk, pv, ldv, ps, M, k_codes.shape[0] * k_codes.shape[1], H, D)
+
+
+def wq_kv_store_int4(k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, k_codes: torch.Tensor,
+                     k_scales: torch.Tensor, k_zeros: torch.Tensor, v_codes: torch.Tensor, v_scales: torch.Tensor,
+                     v_zeros: torch.Tensor, stream=None) -> None:
+    """Quantise the tokens' keys and values (bf16 [M][H][128], any row stride) into the int4 cache that
+    wq_decode_attention_int4 reads, in place: token m goes to sequence slots[m] // T, place slots[m] % T (int64 [M];
+    a slot outside [0, B T) leaves the token out; slots of one call are distinct).  codes [B][T][H][64] uint8,
+    scales and zero-points [B][T][H] bf16."""
+    dev, rows = _store_rows(k, v, slots, k_codes)
+    size = tuple(k_codes.shape[:3])
+    width = (k.shape[2] // 2,)
+    _on(dev, lib().wq_kv_store_int4, stream, *rows,
+        *(_dense_as(t, n, torch.uint8 if n.endswith("codes") else torch.bfloat16,
+                    size + width if n.endswith("codes") else size, dev)
+          for t, n in ((k_codes, "k_codes"), (k_scales, "k_scales"), (k_zeros, "k_zeros"), (v_codes, "v_codes"),
+                       (v_scales, "v_scales"), (v_zeros, "v_zeros"))))
+
+
+def wq_kv_store_fp8(k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, k_codes: torch.Tensor,
+                    k_scale: torch.Tensor, v_codes: torch.Tensor, v_scale: torch.Tensor, stream=None) -> None:
+    """The same for the fp8 (E4M3) cache of wq_decode_attention_fp8: codes [B][T][H][128] uint8, against the
+    tensors' given scales (float32 [1] on the device)."""
+    dev, rows = _store_rows(k, v, slots, k_codes)
+    size = tuple(k_codes.shape[:3]) + (k.shape[2],)
+    _on(dev, lib().wq_kv_store_fp8, stream, *rows, _dense_as(k_codes, "k_codes", torch.uint8, size, dev),
+        _dense_as(k_scale, "k_scale", torch.float32, (1,), dev), _dense_as(v_codes, "v_codes", torch.uint8, size, dev),
+        _dense_as(v_scale, "v_scale", torch.float32, (1,), dev))
+
+
+def wq_prompt_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, starts: torch.Tensor, o=None,
+                        stream=None) -> torch.Tensor:
+    """Causal attention over packed prompts.  q [M][Hq][D], k and v [M][H][D] bf16 on CUDA (D 64 or 128, heads
+    adjacent, any row stride), query head j reading KV head j // (Hq // H); starts int32 [B + 1] on the device:
+    sequence b owns rows starts[b] .. starts[b + 1].  Returns o bf16 [M][Hq][D]; rows of no sequence keep what they
+    held (allocated here: nothing defined)."""
+    dev = q.device
+    pq, ldq = _heads_of(q, "q")
+    M, Hq, D = q.shape
+    pk, ldk = _heads_of(k, "k", dev)
+    H = k.shape[1]
+    if k.shape[0] != M or k.shape[2] != D:
+        raise ValueError("q and k must have the same tokens and head size")
+    pv, ldv = _heads_of(v, "v", dev, k.shape)
+    if starts.dim() != 1 or starts.numel() < 2:
+        raise ValueError("starts must be a 1-D tensor of at least two values")
+    B = starts.numel() - 1
+    o = torch.empty((M, Hq, D), dtype=torch.bfloat16, device=dev) if o is None else o
+    po, ldo = _heads_of(o, "o", dev, (M, Hq, D))
+    _on(dev, lib().wq_prompt_attention, stream, pq, ldq, pk, ldk, pv, ldv,
+        _dense_as(starts, "starts", torch.int32, (B + 1,), dev), B, M, Hq, H, D, po, ldo)
+    return o

@@ -29,6 +29,8 @@ int fail(int status, const char *fmt, ...)
 }
 
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+bool aligned8(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 7u) == 0; }
+bool aligned4(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
 // a * b * c bytes, saturating (the ranges compared below never wrap)
 uint64_t span(int64_t a, int64_t b, int64_t c)
@@ -43,6 +45,35 @@ bool overlap(const void *a, uint64_t an, const void *b, uint64_t bn)
     if (!a || !b || an == 0 || bn == 0) return false;
     const unsigned __int128 a0 = reinterpret_cast<uintptr_t>(a), b0 = reinterpret_cast<uintptr_t>(b);
     return a0 < b0 + bn && b0 < a0 + an;
+}
+
+// Bytes from the first to the last value of `rows` rows of `width` values, ld values apart
+uint64_t strided(int64_t rows, int64_t ld, int64_t width, int64_t size)
+{
+    return span(rows - 1, ld, size) + span(1, width, size);
+}
+
+// `rows` rows of `width` bf16 values, ld values apart: slices of one buffer interleave without sharing a value.
+struct Rows {
+    const void *p;
+    int64_t rows, ld, width;
+};
+
+// Two row sets share a byte.  Sets with the same row distance that both fit a row are compared within the row
+// (columns of one buffer); others by their whole extent.
+bool rows_overlap(const Rows &a, const Rows &b)
+{
+    if (!overlap(a.p, strided(a.rows, a.ld, a.width, 2), b.p, strided(b.rows, b.ld, b.width, 2))) return false;
+    if (a.ld != b.ld) return true;
+    const int64_t pitch = a.ld * 2;
+    int64_t d = (int64_t)((reinterpret_cast<intptr_t>(b.p) - reinterpret_cast<intptr_t>(a.p)) % pitch);
+    if (d < 0) d += pitch;  // b's column behind a's, within one row distance
+    return d < a.width * 2 || d + b.width * 2 > pitch;
+}
+
+bool rows_overlap(const Rows &a, const void *p, uint64_t bytes)
+{
+    return overlap(a.p, strided(a.rows, a.ld, a.width, 2), p, bytes);
 }
 
 int check_launch(const char *what)
@@ -590,6 +621,203 @@ int wq_awq_channel_scales(const double *magnitudes, int64_t K, double alpha, flo
     if (overlap(col_scale, span(K, 4, 1), magnitudes, span(K, 8, 1)))
         return fail(WQ_ERR_ARG, "%s: output overlaps the magnitudes", what);
     wq::launch_channel_scales(magnitudes, K, alpha, col_scale, static_cast<cudaStream_t>(stream));
+    return check_launch(what);
+}
+
+int wq_quantize_int8_tokens(const void *x, int xtype, int64_t M, int64_t K, int64_t ldx, int8_t *q, float *scales,
+                            void *stream)
+{
+    g_last_error.clear();
+    const char *what = "wq_quantize_int8_tokens";
+    if (!x || !q || !scales) return fail(WQ_ERR_ARG, "%s: null pointer", what);
+    if (M <= 0 || K <= 0 || ldx <= 0) return fail(WQ_ERR_ARG, "%s: M, K and ldx must be positive", what);
+    if (xtype != WQ_F32 && xtype != WQ_BF16) return fail(WQ_ERR_UNSUPPORTED, "%s: xtype %d", what, xtype);
+    if (K % 32 != 0 || ldx < K)
+        return fail(WQ_ERR_SHAPE, "%s: need K %% 32 == 0 and ldx >= K (K=%lld ldx=%lld)", what, (long long)K,
+                    (long long)ldx);
+    if (M > 0x7fffffffLL || K > 0x7fffffffLL || ldx > (1LL << 40))
+        return fail(WQ_ERR_SHAPE, "%s: M, K or ldx too large", what);
+    if (ldx % 8 != 0 || !aligned16(x) || !aligned16(q) || !aligned4(scales))
+        return fail(WQ_ERR_ALIGN, "%s: x and q must be 16-byte aligned, scales 4-byte, ldx a multiple of 8", what);
+    const uint64_t es = xtype == WQ_F32 ? 4 : 2, xb = strided(M, ldx, K, es), qb = span(M, K, 1), sb = span(M, 4, 1);
+    if (overlap(q, qb, x, xb) || overlap(scales, sb, x, xb) || overlap(scales, sb, q, qb))
+        return fail(WQ_ERR_ARG, "%s: output buffers overlap x or each other", what);
+    wq::launch_quantize_int8_tokens(x, xtype, M, K, ldx, q, scales, static_cast<cudaStream_t>(stream));
+    return check_launch(what);
+}
+
+size_t wq_gemm_w8a8_int8_workspace_bytes(int64_t M, int64_t N, int64_t K)
+{
+    return wq::gemm_int8_workspace_bytes(M, N, K);
+}
+
+int wq_gemm_w8a8_int8(const int8_t *xq, const float *xscales, int64_t M, int64_t N, int64_t K, const int8_t *qweight,
+                      const uint16_t *scales, uint16_t *y, void *workspace, size_t ws_bytes, void *stream)
+{
+    g_last_error.clear();
+    const char *what = "wq_gemm_w8a8_int8";
+    if (!xq || !xscales || !qweight || !scales || !y) return fail(WQ_ERR_ARG, "%s: null pointer", what);
+    if (M <= 0 || N <= 0 || K <= 0) return fail(WQ_ERR_ARG, "%s: M, N and K must be positive", what);
+    if (K % 32 != 0 || K >= 131072)
+        return fail(WQ_ERR_SHAPE, "%s: need K %% 32 == 0 and K < 131072 (K=%lld)", what, (long long)K);
+    if (M > 0x7fffffffLL || N > 0x7fffffffLL) return fail(WQ_ERR_SHAPE, "%s: M or N too large", what);
+    if (!aligned16(xq) || !aligned16(qweight) || !aligned16(scales) || !aligned16(y) || !aligned4(xscales))
+        return fail(WQ_ERR_ALIGN, "%s: pointers must be 16-byte aligned (xscales 4-byte)", what);
+    const uint64_t yb = span(M, N, 2);
+    if (overlap(y, yb, xq, span(M, K, 1)) || overlap(y, yb, qweight, span(N, K, 1)) ||
+        overlap(y, yb, scales, span(N, 2, 1)) || overlap(y, yb, xscales, span(M, 4, 1)))
+        return fail(WQ_ERR_ARG, "%s: y overlaps an input", what);
+    const size_t need = wq::gemm_int8_workspace_bytes(M, N, K);
+    if (need > 0 && (!workspace || ws_bytes < need || !aligned16(workspace)))
+        return fail(WQ_ERR_WORKSPACE, "%s: need %zu workspace bytes", what, need);
+    if (need > 0 && overlap(workspace, need, y, yb)) return fail(WQ_ERR_ARG, "%s: the workspace overlaps y", what);
+    int *status = status_word();
+    if (!status) return fail(WQ_ERR_CUDA, "%s: no device status word", what);
+    if (wq::launch_gemm_w8a8_int8(xq, xscales, M, N, K, qweight, scales, y, workspace, status,
+                                  static_cast<cudaStream_t>(stream)) != 0)
+        return fail(WQ_ERR_CUDA, "%s: tensor map encoding or workspace clear failed", what);
+    return check_launch(what);
+}
+
+namespace {
+
+// Heads of D values, `heads` of them adjacent per row, rows ld apart, `rows` rows: the checks shared by the calls
+// on queries, keys and values.
+int check_rows(const char *what, const char *name, const void *p, int64_t ld, int64_t heads, int64_t D)
+{
+    if (ld < heads * D) return fail(WQ_ERR_SHAPE, "%s: ld%s < heads * D", what, name);
+    if (ld > (1LL << 40)) return fail(WQ_ERR_SHAPE, "%s: ld%s too large", what, name);
+    if (ld % 8 != 0 || !aligned16(p))
+        return fail(WQ_ERR_ALIGN, "%s: %s must be 16-byte aligned and ld%s a multiple of 8", what, name, name);
+    return WQ_OK;
+}
+
+}  // namespace
+
+int wq_qk_norm_rope(const uint16_t *q, int64_t ldq, const uint16_t *k, int64_t ldk, const uint16_t *q_weight,
+                    const uint16_t *k_weight, float eps, const int32_t *positions, const float *inv_freq, int64_t rot,
+                    int interleaved, int64_t M, int64_t Hq, int64_t H, int64_t D, uint16_t *q_out, int64_t ldq_out,
+                    uint16_t *k_out, int64_t ldk_out, void *stream)
+{
+    g_last_error.clear();
+    const char *what = "wq_qk_norm_rope";
+    if (!q || !k || !positions || !inv_freq || !q_out || !k_out) return fail(WQ_ERR_ARG, "%s: null pointer", what);
+    if (!q_weight != !k_weight) return fail(WQ_ERR_ARG, "%s: one of q_weight and k_weight is null", what);
+    if (M <= 0 || Hq <= 0 || H <= 0 || D <= 0) return fail(WQ_ERR_ARG, "%s: M, Hq, H and D must be positive", what);
+    if (D != 64 && D != 128) return fail(WQ_ERR_UNSUPPORTED, "%s: D must be 64 or 128 (D=%lld)", what, (long long)D);
+    if (rot <= 0 || rot > D || rot % 16 != 0)
+        return fail(WQ_ERR_SHAPE, "%s: rot must be a multiple of 16 in [16, D] (rot=%lld)", what, (long long)rot);
+    if (q_weight && !(eps >= 0.0f)) return fail(WQ_ERR_ARG, "%s: eps must not be negative", what);
+    if (M > 0x7fffffffLL || Hq > 65535 || H > 65535) return fail(WQ_ERR_SHAPE, "%s: M, Hq or H too large", what);
+    int rc;
+    if ((rc = check_rows(what, "q", q, ldq, Hq, D)) != WQ_OK || (rc = check_rows(what, "k", k, ldk, H, D)) != WQ_OK ||
+        (rc = check_rows(what, "q_out", q_out, ldq_out, Hq, D)) != WQ_OK ||
+        (rc = check_rows(what, "k_out", k_out, ldk_out, H, D)) != WQ_OK)
+        return rc;
+    if ((q_weight && (!aligned16(q_weight) || !aligned16(k_weight))) || !aligned4(positions) || !aligned4(inv_freq))
+        return fail(WQ_ERR_ALIGN, "%s: weights must be 16-byte aligned, positions and inv_freq 4-byte", what);
+    const Rows rq{q, M, ldq, Hq * D}, rk{k, M, ldk, H * D}, oq{q_out, M, ldq_out, Hq * D}, ok{k_out, M, ldk_out, H * D};
+    const bool same_q = q_out == q && ldq_out == ldq, same_k = k_out == k && ldk_out == ldk;
+    if ((!same_q && rows_overlap(oq, rq)) || (!same_k && rows_overlap(ok, rk)) || rows_overlap(oq, rk) ||
+        rows_overlap(ok, rq) || rows_overlap(oq, ok) || rows_overlap(oq, positions, span(M, 4, 1)) ||
+        rows_overlap(ok, positions, span(M, 4, 1)) || rows_overlap(oq, inv_freq, 2 * rot) ||
+        rows_overlap(ok, inv_freq, 2 * rot) || rows_overlap(oq, q_weight, 2 * D) || rows_overlap(oq, k_weight, 2 * D) ||
+        rows_overlap(ok, q_weight, 2 * D) || rows_overlap(ok, k_weight, 2 * D))
+        return fail(WQ_ERR_ARG, "%s: an output overlaps an input (other than its own, in place) or the other output", what);
+    wq::launch_qk_norm_rope(q, ldq, k, ldk, q_weight, k_weight, eps, positions, inv_freq, rot, interleaved, M, Hq, H, D,
+                            q_out, ldq_out, k_out, ldk_out, static_cast<cudaStream_t>(stream));
+    return check_launch(what);
+}
+
+namespace {
+
+int check_store(const char *what, bool fp8, const void *k, int64_t ldk, const void *v, int64_t ldv, const void *slots,
+                int64_t M, int64_t S, int64_t H, int64_t D, const void *kc, const void *ks, const void *kz,
+                const void *vc, const void *vs, const void *vz)
+{
+    if (!k || !v || !slots || !kc || !ks || !vc || !vs || (!fp8 && (!kz || !vz)))
+        return fail(WQ_ERR_ARG, "%s: null pointer", what);
+    if (M <= 0 || S <= 0 || H <= 0 || D <= 0) return fail(WQ_ERR_ARG, "%s: M, S, H and D must be positive", what);
+    if (D != 128) return fail(WQ_ERR_UNSUPPORTED, "%s: needs D == 128 (D=%lld)", what, (long long)D);
+    if (H > 65535 || M > 0x7fffffffLL || M * H >= (1LL << 35) || S > (1LL << 40))
+        return fail(WQ_ERR_SHAPE, "%s: M, S or H too large", what);
+    int rc;
+    if ((rc = check_rows(what, "k", k, ldk, H, D)) != WQ_OK || (rc = check_rows(what, "v", v, ldv, H, D)) != WQ_OK)
+        return rc;
+    const bool al = aligned16(kc) && aligned16(vc) && aligned8(slots) &&
+                    (fp8 ? aligned4(ks) && aligned4(vs) : aligned16(ks) && aligned16(kz) && aligned16(vs) && aligned16(vz));
+    if (!al) return fail(WQ_ERR_ALIGN, "%s: cache pointers must be 16-byte aligned (fp8 scales 4-byte, slots 8-byte)", what);
+    const uint64_t cb = span(S, H, fp8 ? D : D / 2), pb = span(S, H, 2), sb = span(M, 8, 1);
+    const Rows rk{k, M, ldk, H * D}, rv{v, M, ldv, H * D};
+    const void *out[6] = {kc, vc, fp8 ? nullptr : ks, fp8 ? nullptr : kz, fp8 ? nullptr : vs, fp8 ? nullptr : vz};
+    const uint64_t bytes[6] = {cb, cb, pb, pb, pb, pb};
+    for (int i = 0; i < 6; ++i) {
+        bool bad = rows_overlap(rk, out[i], bytes[i]) || rows_overlap(rv, out[i], bytes[i]) ||
+                   overlap(out[i], bytes[i], slots, sb) || (fp8 && (overlap(out[i], bytes[i], ks, 4) || overlap(out[i], bytes[i], vs, 4)));
+        for (int j = 0; j < i; ++j) bad = bad || overlap(out[i], bytes[i], out[j], bytes[j]);
+        if (bad) return fail(WQ_ERR_ARG, "%s: a part of the cache overlaps an input or another part", what);
+    }
+    return WQ_OK;
+}
+
+}  // namespace
+
+int wq_kv_store_int4(const uint16_t *k, int64_t ldk, const uint16_t *v, int64_t ldv, const int64_t *slots, int64_t M,
+                     int64_t S, int64_t H, int64_t D, uint8_t *k_codes, uint16_t *k_scales, uint16_t *k_zeros,
+                     uint8_t *v_codes, uint16_t *v_scales, uint16_t *v_zeros, void *stream)
+{
+    g_last_error.clear();
+    const char *what = "wq_kv_store_int4";
+    const int rc = check_store(what, false, k, ldk, v, ldv, slots, M, S, H, D, k_codes, k_scales, k_zeros, v_codes,
+                               v_scales, v_zeros);
+    if (rc != WQ_OK) return rc;
+    wq::launch_kv_store(false, k, ldk, v, ldv, slots, M, S, H, k_codes, k_scales, k_zeros, nullptr, v_codes, v_scales,
+                        v_zeros, nullptr, static_cast<cudaStream_t>(stream));
+    return check_launch(what);
+}
+
+int wq_kv_store_fp8(const uint16_t *k, int64_t ldk, const uint16_t *v, int64_t ldv, const int64_t *slots, int64_t M,
+                    int64_t S, int64_t H, int64_t D, uint8_t *k_codes, const float *k_scale, uint8_t *v_codes,
+                    const float *v_scale, void *stream)
+{
+    g_last_error.clear();
+    const char *what = "wq_kv_store_fp8";
+    const int rc = check_store(what, true, k, ldk, v, ldv, slots, M, S, H, D, k_codes, k_scale, nullptr, v_codes,
+                               v_scale, nullptr);
+    if (rc != WQ_OK) return rc;
+    wq::launch_kv_store(true, k, ldk, v, ldv, slots, M, S, H, k_codes, nullptr, nullptr, k_scale, v_codes, nullptr,
+                        nullptr, v_scale, static_cast<cudaStream_t>(stream));
+    return check_launch(what);
+}
+
+int wq_prompt_attention(const uint16_t *q, int64_t ldq, const uint16_t *k, int64_t ldk, const uint16_t *v, int64_t ldv,
+                        const int32_t *starts, int64_t B, int64_t M, int64_t Hq, int64_t H, int64_t D, uint16_t *o,
+                        int64_t ldo, void *stream)
+{
+    g_last_error.clear();
+    const char *what = "wq_prompt_attention";
+    if (!q || !k || !v || !starts || !o) return fail(WQ_ERR_ARG, "%s: null pointer", what);
+    if (B <= 0 || M <= 0 || Hq <= 0 || H <= 0 || D <= 0)
+        return fail(WQ_ERR_ARG, "%s: B, M, Hq, H and D must be positive", what);
+    if ((D != 64 && D != 128) || Hq % H != 0 || Hq / H > 64)
+        return fail(WQ_ERR_UNSUPPORTED,
+                    "%s: needs D of 64 or 128 and Hq a multiple of H with Hq / H <= 64 (D=%lld H=%lld Hq=%lld)", what,
+                    (long long)D, (long long)H, (long long)Hq);
+    if (M > 0x3fffffffLL || B > 0xffffffLL || H > 65535 || Hq > 65535)
+        return fail(WQ_ERR_SHAPE, "%s: B, M, Hq or H too large", what);
+    int rc;
+    if ((rc = check_rows(what, "q", q, ldq, Hq, D)) != WQ_OK || (rc = check_rows(what, "k", k, ldk, H, D)) != WQ_OK ||
+        (rc = check_rows(what, "v", v, ldv, H, D)) != WQ_OK || (rc = check_rows(what, "o", o, ldo, Hq, D)) != WQ_OK)
+        return rc;
+    if (!aligned4(starts)) return fail(WQ_ERR_ALIGN, "%s: starts must be 4-byte aligned", what);
+    const Rows rq{q, M, ldq, Hq * D}, rk{k, M, ldk, H * D}, rv{v, M, ldv, H * D}, ro{o, M, ldo, Hq * D};
+    if (rows_overlap(ro, rq) || rows_overlap(ro, rk) || rows_overlap(ro, rv) || rows_overlap(ro, starts, span(B + 1, 4, 1)))
+        return fail(WQ_ERR_ARG, "%s: o overlaps an input", what);
+    int *status = status_word();
+    if (!status) return fail(WQ_ERR_CUDA, "%s: no device status word", what);
+    if (wq::launch_prompt_attention(q, ldq, k, ldk, v, ldv, starts, B, M, Hq, H, D, o, ldo, status,
+                                    static_cast<cudaStream_t>(stream)) != 0)
+        return fail(WQ_ERR_CUDA, "%s: tensor map encoding failed", what);
     return check_launch(what);
 }
 

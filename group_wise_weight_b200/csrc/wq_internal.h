@@ -163,6 +163,34 @@ int launch_kv_attn(bool fp8, const uint16_t *q, const uint8_t *kc, const uint16_
                    const int *lengths, int64_t B, int64_t T, int64_t H, int64_t Hq, float *o, void *workspace,
                    cudaStream_t st);
 
+// Per-token INT8 quantiser (wq_quant_tokens.cu): q [M][K], one binary32 scale per row.
+void launch_quantize_int8_tokens(const void *x, int xtype, int64_t M, int64_t K, int64_t ldx, int8_t *q, float *s,
+                                 cudaStream_t st);
+
+// INT8 W8A8 tcgen05 matmul (wq_gemm_lowp.cu): K % 32 == 0, K < 131072.  Workspace as the FP8 matmul's, with
+// 32-bit integer partials.  Returns 0, or -1 if a tensor map cannot be encoded, -2 if a clear fails.
+size_t gemm_int8_workspace_bytes(int64_t M, int64_t N, int64_t K);
+int launch_gemm_w8a8_int8(const int8_t *xq, const float *xscales, int64_t M, int64_t N, int64_t K, const int8_t *wq,
+                          const uint16_t *wscales, uint16_t *y, void *workspace, int *status, cudaStream_t st);
+
+// Per-head norms and rotary positions of queries and keys (wq_rope.cu): D in {64, 128}, rot a multiple of 16.
+// qw, kw: both null for positions alone.
+void launch_qk_norm_rope(const uint16_t *q, int64_t ldq, const uint16_t *k, int64_t ldk, const uint16_t *qw,
+                         const uint16_t *kw, float eps, const int32_t *positions, const float *inv_freq, int64_t rot,
+                         int interleaved, int64_t M, int64_t Hq, int64_t H, int64_t D, uint16_t *qo, int64_t ldqo,
+                         uint16_t *ko, int64_t ldko, cudaStream_t st);
+
+// Keys and values into an int4 or fp8 cache of S rows of H vectors of 128 (wq_kv_store.cu).
+void launch_kv_store(bool fp8, const uint16_t *k, int64_t ldk, const uint16_t *v, int64_t ldv, const int64_t *slots,
+                     int64_t M, int64_t S, int64_t H, uint8_t *kc, uint16_t *ks, uint16_t *kz, const float *k8s,
+                     uint8_t *vc, uint16_t *vs, uint16_t *vz, const float *v8s, cudaStream_t st);
+
+// Causal attention over packed prompts (wq_prompt_attn.cu): D in {64, 128}, Hq / H <= 64.  Returns 0, or -1 if a
+// tensor map cannot be encoded.
+int launch_prompt_attention(const uint16_t *q, int64_t ldq, const uint16_t *k, int64_t ldk, const uint16_t *v,
+                            int64_t ldv, const int32_t *starts, int64_t B, int64_t M, int64_t Hq, int64_t H, int64_t D,
+                            uint16_t *o, int64_t ldo, int *status, cudaStream_t st);
+
 // x_out[m][k] = bf16(x[m][k] / col_scale[k]) (IEEE binary32 quotient), M rows of K (wq_colscale.cu).
 void launch_colscale_x(const uint16_t *x, int64_t M, int64_t K, const float *col_scale, uint16_t *x_out,
                        cudaStream_t st);

@@ -478,6 +478,126 @@ int wq_gemm_w4a16_noalloc(const uint16_t *x, int64_t M, int64_t N, int64_t K, co
                           const uint16_t *scales, const uint16_t *zeros, int g, uint16_t *y, void *stream);
 
 /*
+ * Symmetric INT8 quantisation of activations with one binary32 scale per row
+ * (token): the left operand of wq_gemm_w8a8_int8  ([P3] "What quantisation
+ * does", the scale dynamic and per token).
+ *
+ *   x       [M][ldx] of WQ_F32 or WQ_BF16 (xtype); only the first K columns are read
+ *   q       [M][K] int8 in -127..127;  scales [M] binary32
+ *
+ * Per row, in binary32:
+ *   s = max|x| / 127; if s == 0: s = 1
+ *   q = clip(round(x / s), -127, 127)
+ * Requirements: M >= 1; K >= 32, K % 32 == 0; ldx >= K, ldx % 8 == 0; x and q
+ * 16-byte aligned, scales 4-byte; the outputs must not overlap x or each other
+ * (x's whole rows, columns K .. ldx - 1 included, except in the last row).
+ */
+int wq_quantize_int8_tokens(const void *x, int xtype, int64_t M, int64_t K, int64_t ldx, int8_t *q, float *scales,
+                            void *stream);
+
+/* Bytes of device workspace wq_gemm_w8a8_int8 needs for this shape (contract as wq_gemm_workspace_bytes). */
+size_t wq_gemm_w8a8_int8_workspace_bytes(int64_t M, int64_t N, int64_t K);
+
+/*
+ * INT8 W8A8 matmul on the tensor cores with a scale per token and per output
+ * channel ([P3] "What quantisation does": the products of the codes, scaled).
+ *
+ *   xq, xscales      [M][K] int8 and [M] binary32, as from wq_quantize_int8_tokens
+ *   qweight, scales  [N][K] int8 and [N] bf16, as from wq_quantize_int8 with g = K
+ *   y                [M][N] bf16,
+ *     y[m][n] = bf16( float(sum_k xq[m][k] qweight[n][k]) * (xscales[m] * scales[n]) )
+ * The sum is an exact 32-bit integer (any int8 codes, -128 included: K <
+ * 131072), so y does not depend on the order of the sums, and every operation
+ * after it is binary32, round to nearest even: y is defined bit by bit.
+ * Requirements: M, N >= 1; K >= 32, K % 32 == 0, K < 131072; xq, qweight,
+ * scales, y 16-byte aligned, xscales 4-byte; workspace of
+ * wq_gemm_w8a8_int8_workspace_bytes bytes, not overlapping y; y must not
+ * overlap an input.  Split tiles are combined by the CTA of their first
+ * segment, as described under wq_gemm_w4a16.
+ */
+int wq_gemm_w8a8_int8(const int8_t *xq, const float *xscales, int64_t M, int64_t N, int64_t K, const int8_t *qweight,
+                      const uint16_t *scales, uint16_t *y, void *workspace, size_t ws_bytes, void *stream);
+
+/*
+ * RMS norms of each query and key head and rotary positions, in one pass over
+ * a projection's output.  For token m and a head's D values x:
+ *   n_i = x_i / sqrt(mean(x^2) + eps) * w_i      (x itself when both weights are NULL)
+ *   pairs (a, b) of the first `rot` values turn by the angle positions[m] * inv_freq[i]:
+ *     (a cos - b sin, b cos + a sin); pair i is (i, i + rot/2), or (2i, 2i + 1)
+ *     when `interleaved` is not 0; values rot .. D - 1 are not turned.
+ * Sums, norms and rotations are binary32 (the angle is formed and reduced in
+ * binary64), rounded to bf16 once.
+ *
+ *   q, k             rows of Hq (H) heads of D bf16 values, ldq (ldk) values apart
+ *   q_weight, k_weight  [D] bf16, or both NULL
+ *   positions        [M] int32;  inv_freq [rot / 2] binary32; both on the device
+ *   q_out, k_out     as q and k, with their own row distances; q_out == q with
+ *                    ldq_out == ldq works in place, and so for k
+ * Requirements: M, Hq, H >= 1; D 64 or 128 (WQ_ERR_UNSUPPORTED otherwise);
+ * rot a multiple of 16, 16 <= rot <= D; row distances >= heads * D and
+ * multiples of 8; rows and weights 16-byte aligned, positions and inv_freq
+ * 4-byte; no other overlap of an output with an input or the other output
+ * (columns of one buffer, with the same row distance, are apart).
+ */
+int wq_qk_norm_rope(const uint16_t *q, int64_t ldq, const uint16_t *k, int64_t ldk, const uint16_t *q_weight,
+                    const uint16_t *k_weight, float eps, const int32_t *positions, const float *inv_freq, int64_t rot,
+                    int interleaved, int64_t M, int64_t Hq, int64_t H, int64_t D, uint16_t *q_out, int64_t ldq_out,
+                    uint16_t *k_out, int64_t ldk_out, void *stream);
+
+/*
+ * Store new tokens' keys and values into a quantised KV cache, in the formats
+ * that the decode attention reads ("Quantization for LLM inference ...",
+ * section "KV cache quantization"): int4 vectors exactly as wq_quantize_int4
+ * with g = 128 makes them, fp8 ones as wq_quantize_fp8_tensor encodes against
+ * its scale, here the given one (nearest E4M3 value to k / *k_scale, ties to
+ * the even code, saturated at +-448).
+ *
+ *   k, v      M rows of H heads of D = 128 bf16 values, ldk (ldv) values apart
+ *   slots     [M] int64 on the device: token m goes to vectors slots[m] * H ..
+ *             of the cache viewed as S = B * T rows of H vectors; a slot below 0
+ *             or from S on leaves the token out.  The slots of one call must be
+ *             distinct (those left out may repeat).
+ *   cache     as described under wq_decode_attention_int4 / _fp8; vectors of
+ *             no slot are left as they are
+ *   k_scale, v_scale  one positive binary32 value each, on the device
+ * Requirements: M, S, H >= 1; D == 128 (WQ_ERR_UNSUPPORTED otherwise); ldk,
+ * ldv >= H * D and multiples of 8; rows and cache 16-byte aligned, slots
+ * 8-byte, fp8 scales 4-byte; no part of the cache overlaps an input or another
+ * part.
+ */
+int wq_kv_store_int4(const uint16_t *k, int64_t ldk, const uint16_t *v, int64_t ldv, const int64_t *slots, int64_t M,
+                     int64_t S, int64_t H, int64_t D, uint8_t *k_codes, uint16_t *k_scales, uint16_t *k_zeros,
+                     uint8_t *v_codes, uint16_t *v_scales, uint16_t *v_zeros, void *stream);
+int wq_kv_store_fp8(const uint16_t *k, int64_t ldk, const uint16_t *v, int64_t ldv, const int64_t *slots, int64_t M,
+                    int64_t S, int64_t H, int64_t D, uint8_t *k_codes, const float *k_scale, uint8_t *v_codes,
+                    const float *v_scale, void *stream);
+
+/*
+ * Causal attention over whole prompts packed one after another.  Sequence b
+ * owns rows starts[b] .. starts[b + 1] - 1; its token t attends to its tokens
+ * u <= t:
+ *   score_u = (q_tj . k_u) / sqrt(D), p = softmax(score), o_tj = sum_u p_u v_u,
+ *   query head j reading KV head j / (Hq / H).
+ *
+ *   q, k, v   rows of Hq (H, H) heads of D bf16 values, ldq (ldk, ldv) values apart
+ *   starts    [B + 1] int32 on the device, not decreasing, within 0 .. M;
+ *             sequences may be empty
+ *   o         rows of Hq heads of D bf16 values, ldo apart; rows of no sequence
+ *             (before starts[0], from starts[B] on) are left as they were, and
+ *             what q, k and v hold there (infinities and NaN too) changes nothing
+ * Scores, the running maximum and sum and the accumulator are binary32; p
+ * is rounded to bf16 as the second product's operand, o once.  Repeated calls
+ * give identical bytes.
+ * Requirements: B, M >= 1; D 64 or 128, Hq % H == 0, Hq / H <= 64
+ * (WQ_ERR_UNSUPPORTED otherwise); row distances >= heads * D and multiples of
+ * 8; q, k, v, o 16-byte aligned, starts 4-byte; o must not overlap an input
+ * (columns of one buffer, with the same row distance, are apart).
+ */
+int wq_prompt_attention(const uint16_t *q, int64_t ldq, const uint16_t *k, int64_t ldk, const uint16_t *v, int64_t ldv,
+                        const int32_t *starts, int64_t B, int64_t M, int64_t Hq, int64_t H, int64_t D, uint16_t *o,
+                        int64_t ldo, void *stream);
+
+/*
  * Device status word.  Kernels with waits on barriers bound every wait; a
  * wait that runs out records a code on the device and the kernel returns
  * early instead of hanging.  This call synchronises `stream`, returns
