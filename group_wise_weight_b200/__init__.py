@@ -154,8 +154,8 @@ def _check(rc: int):
 
 
 def _stream_handle(stream) -> int:
-    if stream is None:
-        stream = torch.cuda.current_stream()
+    if stream is None:  # the handle alone: building a Stream object costs more than a launch
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     return int(stream.cuda_stream) if hasattr(stream, "cuda_stream") else int(stream)
 
 
@@ -567,12 +567,20 @@ def _dense_as(t: torch.Tensor, name: str, dtype, shape, device) -> int:
     ptr = _dev(t, name)
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}")
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
     if t.device != device:
         raise ValueError(f"{name} is on {t.device}, not on {device}")
     _dense(t, name)
     return ptr
+
+
+def _out(t, name: str, dtype, shape, like: torch.Tensor):
+    """(tensor, address) of an output: the given one, checked, or a new one on like's device."""
+    if t is None:
+        t = like.new_empty(shape, dtype=dtype)
+        return t, t.data_ptr()
+    return t, _dense_as(t, name, dtype, shape, like.device)
 
 
 def _heads_of(t: torch.Tensor, name: str, device=None, shape=None):
@@ -582,12 +590,21 @@ def _heads_of(t: torch.Tensor, name: str, device=None, shape=None):
         raise TypeError(f"{name} must be a 3-D bfloat16 tensor [tokens][heads][D]")
     if device is not None and t.device != device:
         raise ValueError(f"{name} is on {t.device}, not on {device}")
-    if shape is not None and tuple(t.shape) != tuple(shape):
+    if shape is not None and t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
     M, H, D = t.shape
-    if (D > 1 and t.stride(2) != 1) or (H > 1 and t.stride(1) != D):
+    ld, head, one = t.stride()
+    if (D > 1 and one != 1) or (H > 1 and head != D):
         raise ValueError(f"{name} must hold each token's heads one after another (strides D and 1)")
-    return ptr, (t.stride(0) if M > 1 else H * D)
+    return ptr, (ld if M > 1 else H * D)
+
+
+def _heads_out(t, name: str, shape, like: torch.Tensor):
+    """(tensor, address, row distance) of an output of heads: the given one, checked, or a new dense one."""
+    if t is None:
+        t = like.new_empty(shape)
+        return t, t.data_ptr(), shape[1] * shape[2]
+    return (t, *_heads_of(t, name, like.device, shape))
 
 
 def wq_quantize_int8_tokens(x: torch.Tensor, q=None, scales=None, stream=None):
@@ -599,10 +616,9 @@ def wq_quantize_int8_tokens(x: torch.Tensor, q=None, scales=None, stream=None):
         raise ValueError("x must be a 2-D tensor with unit stride along K")
     xtype = _wtype(x)
     M, K = x.shape
-    q = torch.empty((M, K), dtype=torch.int8, device=x.device) if q is None else q
-    scales = torch.empty((M,), dtype=torch.float32, device=x.device) if scales is None else scales
-    _on(x.device, lib().wq_quantize_int8_tokens, stream, px, xtype, M, K, x.stride(0) if M > 1 else K,
-        _dense_as(q, "q", torch.int8, (M, K), x.device), _dense_as(scales, "scales", torch.float32, (M,), x.device))
+    q, pq = _out(q, "q", torch.int8, (M, K), x)
+    scales, ps = _out(scales, "scales", torch.float32, (M,), x)
+    _on(x.device, lib().wq_quantize_int8_tokens, stream, px, xtype, M, K, x.stride(0) if M > 1 else K, pq, ps)
     return q, scales
 
 
@@ -621,7 +637,7 @@ def wq_gemm_w8a8_int8(xq: torch.Tensor, xscales: torch.Tensor, qweight: torch.Te
     _dense(xq, "xq")
     M, K = xq.shape
     N = qweight.shape[0]
-    y = torch.empty((M, N), dtype=torch.bfloat16, device=dev) if y is None else y
+    y, py = _out(y, "y", torch.bfloat16, (M, N), xq)
     if workspace is None:
         with torch.cuda.device(dev):
             need = wq_gemm_w8a8_int8_workspace_bytes(M, N, K)
@@ -632,8 +648,7 @@ def wq_gemm_w8a8_int8(xq: torch.Tensor, xscales: torch.Tensor, qweight: torch.Te
     _on(dev, lib().wq_gemm_w8a8_int8, stream, pxq, _dense_as(xscales, "xscales", torch.float32, (M,), dev), M, N, K,
         _dense_as(qweight, "qweight", torch.int8, (N, K), dev),
         _dense_as(scales, "scales", torch.bfloat16, (N,) if scales.dim() == 1 else (N, 1), dev),
-        _dense_as(y, "y", torch.bfloat16, (M, N), dev), _dev(workspace, "workspace"),
-        workspace.numel() * workspace.element_size())
+        py, _dev(workspace, "workspace"), workspace.numel() * workspace.element_size())
     return y
 
 
@@ -654,10 +669,8 @@ def wq_qk_norm_rope(q: torch.Tensor, k: torch.Tensor, positions: torch.Tensor, i
         raise ValueError("q and k must have the same tokens and head size")
     if inv_freq.dim() != 1:
         raise ValueError("inv_freq must be a 1-D tensor")
-    q_out = torch.empty((M, Hq, D), dtype=torch.bfloat16, device=dev) if q_out is None else q_out
-    k_out = torch.empty((M, H, D), dtype=torch.bfloat16, device=dev) if k_out is None else k_out
-    pqo, ldqo = _heads_of(q_out, "q_out", dev, (M, Hq, D))
-    pko, ldko = _heads_of(k_out, "k_out", dev, (M, H, D))
+    q_out, pqo, ldqo = _heads_out(q_out, "q_out", (M, Hq, D), q)
+    k_out, pko, ldko = _heads_out(k_out, "k_out", (M, H, D), k)
     half = inv_freq.numel()
     _on(dev, lib().wq_qk_norm_rope, stream, pq, ldq, pk, ldk,
         None if q_weight is None else _dense_as(q_weight, "q_weight", torch.bfloat16, (D,), dev),
@@ -689,11 +702,11 @@ def wq_kv_store_int4(k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, k_co
     dev, rows = _store_rows(k, v, slots, k_codes)
     size = tuple(k_codes.shape[:3])
     width = (k.shape[2] // 2,)
-    _on(dev, lib().wq_kv_store_int4, stream, *rows,
-        *(_dense_as(t, n, torch.uint8 if n.endswith("codes") else torch.bfloat16,
-                    size + width if n.endswith("codes") else size, dev)
-          for t, n in ((k_codes, "k_codes"), (k_scales, "k_scales"), (k_zeros, "k_zeros"), (v_codes, "v_codes"),
-                       (v_scales, "v_scales"), (v_zeros, "v_zeros"))))
+    u8, bf = torch.uint8, torch.bfloat16
+    _on(dev, lib().wq_kv_store_int4, stream, *rows, _dense_as(k_codes, "k_codes", u8, size + width, dev),
+        _dense_as(k_scales, "k_scales", bf, size, dev), _dense_as(k_zeros, "k_zeros", bf, size, dev),
+        _dense_as(v_codes, "v_codes", u8, size + width, dev), _dense_as(v_scales, "v_scales", bf, size, dev),
+        _dense_as(v_zeros, "v_zeros", bf, size, dev))
 
 
 def wq_kv_store_fp8(k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, k_codes: torch.Tensor,
@@ -724,8 +737,7 @@ def wq_prompt_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, start
     if starts.dim() != 1 or starts.numel() < 2:
         raise ValueError("starts must be a 1-D tensor of at least two values")
     B = starts.numel() - 1
-    o = torch.empty((M, Hq, D), dtype=torch.bfloat16, device=dev) if o is None else o
-    po, ldo = _heads_of(o, "o", dev, (M, Hq, D))
+    o, po, ldo = _heads_out(o, "o", (M, Hq, D), q)
     _on(dev, lib().wq_prompt_attention, stream, pq, ldq, pk, ldk, pv, ldv,
         _dense_as(starts, "starts", torch.int32, (B + 1,), dev), B, M, Hq, H, D, po, ldo)
     return o
