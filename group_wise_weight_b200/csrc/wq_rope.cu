@@ -13,11 +13,16 @@
 // a turn in binary64 before the binary32 sine and cosine, so far positions
 // keep their phase.
 //
-// The pass reads and writes 2 bytes per value and is bound by HBM.  D / 8
-// lanes hold a vector (16-byte loads and stores; the sum of squares is a
-// shuffle over them, the pair's other half of the split form one more), a CTA
-// takes one token or a few, and its sines and cosines are formed once for all
-// heads while the first loads are in flight.
+// The pass reads and writes 2 bytes per value and should be bound by HBM; the
+// first form (a lane's pair partner in another lane, tables in shared memory)
+// was bound by its instructions instead.  Here a lane holds both members of
+// its four pairs -- 4 values of each half, or 8 adjacent ones when interleaved
+// -- so no value crosses lanes but the sum of squares, and the products of
+// weights, cosines and sines that its values meet stay in registers for all
+// heads of a token:
+//   y_a = inv (a (w_a cos) - b (w_b sin)),  y_b = inv (b (w_b cos) + a (w_a sin)).
+// A warp takes 256 / D heads of one token at a time, kUnroll loads in flight;
+// where tokens are few a token's heads are shared out to several warps.
 #include <algorithm>
 
 #include "wq_common.cuh"
@@ -28,9 +33,9 @@ namespace wq {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kUnroll = 4;      // vectors in flight per lane group
-constexpr int kMaxTokens = 16;  // tokens per CTA
-constexpr int kMaxHalf = 64;    // rotated pairs
+constexpr int kWarps = kThreads / 32;
+constexpr int kUnroll = 4;   // loads in flight per lane
+constexpr int kMaxHalf = 64; // rotated pairs
 
 struct RopeArgs {
     const uint16_t *q, *k, *qw, *kw;
@@ -38,113 +43,149 @@ struct RopeArgs {
     const int32_t *positions;
     const float *inv_freq;
     float eps;
-    int half, Hq, H, tokens;  // tokens per CTA
+    int half, Hq, H, split;  // split: warps per token
     uint16_t *qo, *ko;
 };
+
+struct Pairs {
+    f32x2 a[2], b[2];  // the first and second members of four pairs
+};
+
+template <bool INTERLEAVED>
+__device__ __forceinline__ Pairs unpack(const uint2 &u, const uint2 &v)
+{
+    const float x0 = __uint_as_float(u.x << 16), x1 = __uint_as_float(u.x & 0xffff0000u);
+    const float x2 = __uint_as_float(u.y << 16), x3 = __uint_as_float(u.y & 0xffff0000u);
+    const float x4 = __uint_as_float(v.x << 16), x5 = __uint_as_float(v.x & 0xffff0000u);
+    const float x6 = __uint_as_float(v.y << 16), x7 = __uint_as_float(v.y & 0xffff0000u);
+    return INTERLEAVED ? Pairs{{{x0, x2}, {x4, x6}}, {{x1, x3}, {x5, x7}}} : Pairs{{{x0, x1}, {x2, x3}}, {{x4, x5}, {x6, x7}}};
+}
+
+__device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b)
+{
+    f32x2 r;
+    asm("{\n\t.reg .b64 ra, rb, rd;\n\tmov.b64 ra, {%2, %3};\n\tmov.b64 rb, {%4, %5};\n\t"
+        "mul.rn.f32x2 rd, ra, rb;\n\tmov.b64 {%0, %1}, rd;\n\t}"
+        : "=f"(r.x), "=f"(r.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return r;
+}
+
+// The heads base + g, base + g + step, ... below `heads` of one token's queries (or keys), g the lane's group in the
+// warp: src and dst at the token's row; o1, o2 the places of this lane's two groups of 4 values in a head.
+template <int D, bool INTERLEAVED, bool NORM>
+__device__ __forceinline__ void turn_heads(const uint16_t *src, uint16_t *dst, int base, int g, int step, int heads,
+                                           int o1, int o2, const uint16_t *weight, const float c[4], const float s[4], float eps)
+{
+    constexpr int L = D / 8;  // lanes per head
+    float wa[4], wb[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) wa[i] = wb[i] = 1.0f;
+    if (NORM) {
+        const Pairs w = unpack<INTERLEAVED>(__ldg(reinterpret_cast<const uint2 *>(weight + o1)),
+                                            __ldg(reinterpret_cast<const uint2 *>(weight + o2)));
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            wa[2 * i] = w.a[i].x; wa[2 * i + 1] = w.a[i].y;
+            wb[2 * i] = w.b[i].x; wb[2 * i + 1] = w.b[i].y;
+        }
+    }
+    f32x2 ac[2], as[2], bc[2], bs[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        ac[i] = f32x2{wa[2 * i] * c[2 * i], wa[2 * i + 1] * c[2 * i + 1]};
+        as[i] = f32x2{wa[2 * i] * s[2 * i], wa[2 * i + 1] * s[2 * i + 1]};
+        bc[i] = f32x2{wb[2 * i] * c[2 * i], wb[2 * i + 1] * c[2 * i + 1]};
+        bs[i] = f32x2{-wb[2 * i] * s[2 * i], -wb[2 * i + 1] * s[2 * i + 1]};
+    }
+    for (; base < heads; base += step * kUnroll) {
+        uint2 u[kUnroll], v[kUnroll];
+#pragma unroll
+        for (int e = 0; e < kUnroll; ++e) {
+            const int h = base + g + e * step;
+            u[e] = v[e] = make_uint2(0u, 0u);
+            if (h < heads) {
+                if (INTERLEAVED) {
+                    const uint4 x = *reinterpret_cast<const uint4 *>(src + h * D + o1);
+                    u[e] = make_uint2(x.x, x.y);
+                    v[e] = make_uint2(x.z, x.w);
+                } else {
+                    u[e] = *reinterpret_cast<const uint2 *>(src + h * D + o1);
+                    v[e] = *reinterpret_cast<const uint2 *>(src + h * D + o2);
+                }
+            }
+        }
+#pragma unroll
+        for (int e = 0; e < kUnroll; ++e) {
+            const int h = base + g + e * step;
+            const Pairs x = unpack<INTERLEAVED>(u[e], v[e]);
+            f32x2 ya[2], yb[2];
+            float inv = 1.0f;
+            if (NORM) {
+                f32x2 ss = mul2(x.a[0], x.a[0]);
+                ss = fma2_pairs(x.a[1], x.a[1], ss);
+                ss = fma2_pairs(x.b[0], x.b[0], ss);
+                ss = fma2_pairs(x.b[1], x.b[1], ss);
+                float sum = ss.x + ss.y;
+#pragma unroll
+                for (int o = 1; o < L; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+                inv = rsqrtf(fmaf(sum, 1.0f / D, eps));
+            }
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                ya[i] = fma2_pairs(x.b[i], bs[i], mul2(x.a[i], ac[i]));
+                yb[i] = fma2_pairs(x.a[i], as[i], mul2(x.b[i], bc[i]));
+                if (NORM) {
+                    ya[i] = mul2(ya[i], f32x2{inv, inv});
+                    yb[i] = mul2(yb[i], f32x2{inv, inv});
+                }
+            }
+            if (h < heads) {
+                if (INTERLEAVED) {
+                    *reinterpret_cast<uint4 *>(dst + h * D + o1) =
+                        make_uint4(pack_bf16x2(ya[0].x, yb[0].x), pack_bf16x2(ya[0].y, yb[0].y),
+                                   pack_bf16x2(ya[1].x, yb[1].x), pack_bf16x2(ya[1].y, yb[1].y));
+                } else {
+                    *reinterpret_cast<uint2 *>(dst + h * D + o1) = make_uint2(pack_bf16x2(ya[0].x, ya[0].y), pack_bf16x2(ya[1].x, ya[1].y));
+                    *reinterpret_cast<uint2 *>(dst + h * D + o2) = make_uint2(pack_bf16x2(yb[0].x, yb[0].y), pack_bf16x2(yb[1].x, yb[1].y));
+                }
+            }
+        }
+    }
+}
 
 template <int D, bool INTERLEAVED, bool NORM>
 __global__ void __launch_bounds__(kThreads)
 qk_norm_rope_kernel(const RopeArgs p)
 {
-    constexpr int L = D / 8;  // lanes per vector
-    __shared__ __align__(16) float cs[kMaxTokens * kMaxHalf], sn[kMaxTokens * kMaxHalf];
-    const int tid = threadIdx.x, l = tid % L;
-    const int64_t m0 = (int64_t)blockIdx.x * p.tokens;
-    const int nt = (int)std::min<int64_t>(p.tokens, p.M - m0);
-    const int vecs = p.Hq + p.H, total = nt * vecs * L;
-
-    for (int base = 0; base < total; base += kThreads * kUnroll) {
-        uint4 raw[kUnroll];
-        int tok[kUnroll], head[kUnroll];
-#pragma unroll
-        for (int u = 0; u < kUnroll; ++u) {
-            const int idx = base + u * kThreads + tid;
-            const int vec = idx / L;
-            tok[u] = vec / vecs;
-            head[u] = vec - tok[u] * vecs;
-            raw[u] = make_uint4(0u, 0u, 0u, 0u);
-            if (idx < total) {
-                const int64_t m = m0 + tok[u];
-                const uint16_t *src = head[u] < p.Hq ? p.q + m * p.ldq + head[u] * D : p.k + m * p.ldk + (head[u] - p.Hq) * D;
-                raw[u] = *reinterpret_cast<const uint4 *>(src + l * 8);
-            }
-        }
-        if (base == 0) {
-            for (int i = tid; i < nt * p.half; i += kThreads) {
-                const int t = i / p.half, f = i - t * p.half;
-                const double turns = (double)p.positions[m0 + t] * (double)p.inv_freq[f] * 0.15915494309189535;  // / 2 pi
-                const float part = (float)(2.0 * (turns - rint(turns)));
-                sincospif(part, &sn[t * kMaxHalf + f], &cs[t * kMaxHalf + f]);
-            }
-            __syncthreads();
-        }
-#pragma unroll
-        for (int u = 0; u < kUnroll; ++u) {
-            const int idx = base + u * kThreads + tid;
-            const bool is_q = head[u] < p.Hq;
-            float x[8];
-            const uint32_t w4[4] = {raw[u].x, raw[u].y, raw[u].z, raw[u].w};
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                x[2 * i] = __uint_as_float(w4[i] << 16);
-                x[2 * i + 1] = __uint_as_float(w4[i] & 0xffff0000u);
-            }
-            if (NORM) {
-                float ss = 0.0f;
-#pragma unroll
-                for (int i = 0; i < 8; ++i) ss = fmaf(x[i], x[i], ss);
-#pragma unroll
-                for (int o = 1; o < L; o <<= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-                const float inv = 1.0f / sqrtf(ss * (1.0f / D) + p.eps);
-                const uint4 wv = __ldg(reinterpret_cast<const uint4 *>((is_q ? p.qw : p.kw) + l * 8));
-                const uint32_t ww[4] = {wv.x, wv.y, wv.z, wv.w};
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    x[2 * i] = x[2 * i] * inv * __uint_as_float(ww[i] << 16);
-                    x[2 * i + 1] = x[2 * i + 1] * inv * __uint_as_float(ww[i] & 0xffff0000u);
-                }
-            }
-            // lanes past `total` hold tok up to a CTA's worth too far: keep their table reads inside it
-            const int t = idx < total ? tok[u] : 0;
-            float y[8];
-            if (INTERLEAVED) {
-                const bool turned = l * 4 < p.half;
-                const int f = turned ? l * 4 : 0;
-                const float4 c = *reinterpret_cast<const float4 *>(&cs[t * kMaxHalf + f]);
-                const float4 s = *reinterpret_cast<const float4 *>(&sn[t * kMaxHalf + f]);
-                const float cc[4] = {c.x, c.y, c.z, c.w}, ss[4] = {s.x, s.y, s.z, s.w};
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    y[2 * i] = turned ? x[2 * i] * cc[i] - x[2 * i + 1] * ss[i] : x[2 * i];
-                    y[2 * i + 1] = turned ? x[2 * i + 1] * cc[i] + x[2 * i] * ss[i] : x[2 * i + 1];
-                }
-            } else {
-                const int hl = p.half / 8;  // lanes per half
-                const bool turned = l < 2 * hl, second = turned && l >= hl;
-                const int lane = tid & 31;
-                const int other = turned ? (second ? lane - hl : lane + hl) : lane;
-                const int f = turned ? (second ? l - hl : l) * 8 : 0;
-                const float4 c0 = *reinterpret_cast<const float4 *>(&cs[t * kMaxHalf + f]);
-                const float4 c1 = *reinterpret_cast<const float4 *>(&cs[t * kMaxHalf + f + 4]);
-                const float4 s0 = *reinterpret_cast<const float4 *>(&sn[t * kMaxHalf + f]);
-                const float4 s1 = *reinterpret_cast<const float4 *>(&sn[t * kMaxHalf + f + 4]);
-                const float cc[8] = {c0.x, c0.y, c0.z, c0.w, c1.x, c1.y, c1.z, c1.w};
-                const float ss[8] = {s0.x, s0.y, s0.z, s0.w, s1.x, s1.y, s1.z, s1.w};
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const float o = __shfl_sync(0xffffffffu, x[i], other);
-                    // first half: a cos - b sin with b the other lane's; second: b cos + a sin
-                    y[i] = turned ? fmaf(x[i], cc[i], (second ? o : -o) * ss[i]) : x[i];
-                }
-            }
-            if (idx < total) {
-                const int64_t m = m0 + tok[u];
-                uint16_t *dst = is_q ? p.qo + m * p.ldqo + head[u] * D : p.ko + m * p.ldko + (head[u] - p.Hq) * D;
-                *reinterpret_cast<uint4 *>(dst + l * 8) =
-                    make_uint4(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]), pack_bf16x2(y[4], y[5]), pack_bf16x2(y[6], y[7]));
-            }
-        }
+    constexpr int L = D / 8, kHeads = 32 / L;  // heads per warp at a time
+    __shared__ __align__(16) float table[kWarps][2][kMaxHalf];
+    const int wid = threadIdx.x >> 5, lane = threadIdx.x & 31, l = lane % L, g = lane / L;
+    const int64_t task = (int64_t)blockIdx.x * kWarps + wid;
+    const int64_t m = task / p.split;
+    const int part = (int)(task - m * p.split);
+    if (m >= p.M) return;
+    const double pos = (double)p.positions[m];
+    for (int f = lane; f < p.half; f += 32) {
+        const double turns = pos * (double)p.inv_freq[f] * 0.15915494309189535;  // / 2 pi
+        sincospif((float)(2.0 * (turns - rint(turns))), &table[wid][1][f], &table[wid][0][f]);
     }
+    __syncwarp();
+    // lane l holds the pairs 4 l .. 4 l + 3; past the rotated ones, 8 values that do not turn
+    const bool turned = 4 * l < p.half;
+    const int o1 = INTERLEAVED ? 8 * l : turned ? 4 * l : 8 * l;
+    const int o2 = INTERLEAVED ? 8 * l + 4 : turned ? p.half + 4 * l : 8 * l + 4;
+    float c[4] = {1.0f, 1.0f, 1.0f, 1.0f}, s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    if (turned) {
+        const float4 cv = *reinterpret_cast<const float4 *>(&table[wid][0][4 * l]);
+        const float4 sv = *reinterpret_cast<const float4 *>(&table[wid][1][4 * l]);
+        c[0] = cv.x; c[1] = cv.y; c[2] = cv.z; c[3] = cv.w;
+        s[0] = sv.x; s[1] = sv.y; s[2] = sv.z; s[3] = sv.w;
+    }
+    const int step = p.split * kHeads;
+    turn_heads<D, INTERLEAVED, NORM>(p.q + m * p.ldq, p.qo + m * p.ldqo, part * kHeads, g, step, p.Hq, o1, o2, p.qw, c, s, p.eps);
+    // the keys from the other end, so that the warps with fewer query heads take them
+    turn_heads<D, INTERLEAVED, NORM>(p.k + m * p.ldk, p.ko + m * p.ldko, (p.split - 1 - part) * kHeads, g, step, p.H, o1, o2, p.kw, c, s, p.eps);
 }
 
 template <int D, bool INTERLEAVED>
@@ -162,10 +203,10 @@ void launch_qk_norm_rope(const uint16_t *q, int64_t ldq, const uint16_t *k, int6
                          uint16_t *ko, int64_t ldko, cudaStream_t st)
 {
     RopeArgs a{q, k, qw, kw, ldq, ldk, ldqo, ldko, M, positions, inv_freq, eps, (int)(rot / 2), (int)Hq, (int)H, 1, qo, ko};
-    // a few tokens per CTA where a token is small, as long as every SM keeps a few CTAs
-    const int64_t lanes = (Hq + H) * (D / 8);
-    a.tokens = (int)std::max<int64_t>(1, std::min<int64_t>({kMaxTokens, kThreads * kUnroll / lanes, M / 592}));
-    const unsigned grid = (unsigned)((M + a.tokens - 1) / a.tokens);
+    // one warp per token once that fills the device (148 SMs x 32 warps), else a token's heads over more of them
+    const int64_t at_once = 256 / D, turns = (Hq + at_once - 1) / at_once;
+    a.split = (int)std::max<int64_t>(1, std::min<int64_t>(turns, 148 * 32 / M));
+    const unsigned grid = (unsigned)((M * a.split + kWarps - 1) / kWarps);
     if (D == 128) {
         if (interleaved) run<128, true>(a, grid, st);
         else run<128, false>(a, grid, st);
