@@ -739,7 +739,7 @@ int check_store(const char *what, bool fp8, const void *k, int64_t ldk, const vo
         return fail(WQ_ERR_ARG, "%s: null pointer", what);
     if (M <= 0 || S <= 0 || H <= 0 || D <= 0) return fail(WQ_ERR_ARG, "%s: M, S, H and D must be positive", what);
     if (D != 128) return fail(WQ_ERR_UNSUPPORTED, "%s: needs D == 128 (D=%lld)", what, (long long)D);
-    if (H > 65535 || M > 0x7fffffffLL || M * H >= (1LL << 35) || S > (1LL << 40))
+    if (H > 65535 || M > 0x7fffffffLL || M * H >= (1LL << 30) || S > (1LL << 40))
         return fail(WQ_ERR_SHAPE, "%s: M, S or H too large", what);
     int rc;
     if ((rc = check_rows(what, "k", k, ldk, H, D)) != WQ_OK || (rc = check_rows(what, "v", v, ldv, H, D)) != WQ_OK)

@@ -15,10 +15,13 @@
 // slot outside [0, B T) leaves the token out.
 //
 // Each value is read once (2 bytes) and written once (0.53 or 1 byte): an HBM
-// stream.  16 lanes take a vector, 8 values each; the int4 minimum and
-// maximum travel as one bf16 pair (min, -max) through four shuffles.
-// Quotients come from a reciprocal (wq_quotient.cuh): one correction step for
-// the bf16 scales of int4, two for the arbitrary binary32 scale of fp8.
+// stream, if the instructions stay few.  8 lanes take a vector, 16 values
+// each, so the block's parameters are formed once per 16 values; the int4
+// minimum and maximum travel as one bf16 pair (min, -max) through three
+// shuffles.  Quotients come from a reciprocal, two per instruction
+// (wq_quotient.cuh): one correction step for the bf16 scales of int4, two for
+// the arbitrary binary32 scale of fp8; blocks outside the proven range use
+// the IEEE division.
 #include <algorithm>
 
 #include "wq_internal.h"
@@ -29,9 +32,10 @@ namespace wq {
 namespace {
 
 constexpr int kD = 128;
-constexpr int kLanes = kD / 8;   // lanes per vector
+constexpr int kLanes = kD / 16;  // lanes per vector
 constexpr int kThreads = 256;
-constexpr int kUnroll = 4;       // vectors in flight per group of 16 lanes
+constexpr int kGroups = kThreads / kLanes;
+constexpr int kUnroll = 2;       // vectors in flight per group of 8 lanes
 
 struct StoreArgs {
     const uint16_t *k, *v;
@@ -44,111 +48,152 @@ struct StoreArgs {
     const float *k8s, *v8s;       // fp8
 };
 
-// The vector's int4 block: this lane's 8 codes as one word, and s and z.
-__device__ __forceinline__ uint32_t int4_block(const uint4 &raw, float &s, float &z)
+// Pair i of a lane's 16 values, widened to binary32.
+__device__ __forceinline__ uint64_t pair_of(const uint4 raw[2], int i)
 {
-    const uint32_t lo = bf16x2_min(bf16x2_min(raw.x, raw.y), bf16x2_min(raw.z, raw.w));
-    const uint32_t hi = bf16x2_max(bf16x2_max(raw.x, raw.y), bf16x2_max(raw.z, raw.w)) ^ 0x80008000u;
+    const uint32_t w = word_of(raw[i >> 2], i & 3);
+    return ((uint64_t)(w & 0xffff0000u) << 32) | (uint64_t)(w << 16);
+}
+__device__ __forceinline__ float lo_of(uint64_t p) { return __uint_as_float((uint32_t)p); }
+__device__ __forceinline__ float hi_of(uint64_t p) { return __uint_as_float((uint32_t)(p >> 32)); }
+
+// The vector's int4 block: this lane's 16 codes, and s and z.
+__device__ __forceinline__ uint2 int4_block(const uint4 raw[2], float &s, float &z)
+{
+    uint32_t lo = raw[0].x, hi = raw[0].x;
+#pragma unroll
+    for (int i = 1; i < 8; ++i) {
+        lo = bf16x2_min(lo, word_of(raw[i >> 2], i & 3));
+        hi = bf16x2_max(hi, word_of(raw[i >> 2], i & 3));
+    }
+    hi ^= 0x80008000u;
     uint32_t pk = bf16x2_min(__byte_perm(lo, hi, 0x5410), __byte_perm(lo, hi, 0x7632));
 #pragma unroll
     for (int o = 1; o < kLanes; o <<= 1) pk = bf16x2_min(pk, __shfl_xor_sync(0xffffffffu, pk, o));
     const float mn = __uint_as_float(pk << 16), mx = __uint_as_float((pk & 0xffff0000u) ^ 0x80000000u);
     s = int4_scale(mn, mx);
-    const bool fast = quotients_by_reciprocal(s, fmaxf(fabsf(mn), fabsf(mx)));
-    const float r = __frcp_rn(s);
-    const float zq = fast ? quotient_rn(-mn, s, r) : __fdiv_rn(-mn, s);
-    z = round_bf16(__fadd_rn(rintf(zq), 0.0f));
-    uint32_t packed = 0u - kRintBase * 0x11111111u;
+    const float maxabs = fmaxf(fabsf(mn), fabsf(mx));
+    uint32_t code[2];
+    if (quotients_by_reciprocal(s, maxabs) && maxabs <= s * 8192.0f) {
+        const float r = __frcp_rn(s);
+        z = round_bf16(__fadd_rn(rintf(quotient_rn(-mn, s, r)), 0.0f));
+        // |w / s + z| < 2^15: the integer rounded by 1.5 * 2^23 is the low half-word of its pattern
+        const uint64_t r2 = f32x2_bits(r, r), ns2 = f32x2_bits(-s, -s), z2 = f32x2_bits(z, z);
+        const uint64_t m2 = f32x2_bits(0x1.8p23f, 0x1.8p23f);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const uint32_t word = word_of(raw, i >> 1);
-        const float w = __uint_as_float((i & 1) ? (word & 0xffff0000u) : (word << 16));
-        const float t = __fadd_rn(fast ? quotient_rn(w, s, r) : __fdiv_rn(w, s), z);
-        packed += rint_bits(fminf(fmaxf(t, 0.0f), 15.0f)) << (4 * i);
-    }
-    return packed;
-}
-
-// This lane's 8 E4M3 codes against the tensor's scale s (r = RN(1 / s) when `fast`).
-__device__ __forceinline__ uint2 fp8_codes(const uint4 &raw, float s, float r, bool fast)
-{
-    uint32_t c[4];
-    const float top = __fmul_rn(s, 1024.0f);  // |w / s| >= 1024 saturates all the same
+        for (int j = 0; j < 2; ++j) {
+            uint32_t b[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const uint32_t word = word_of(raw, i);
-        float q[2];
+            for (int i = 0; i < 4; ++i) {
+                const uint64_t w = pair_of(raw, 4 * j + i), q0 = f32x2_mul(w, r2);
+                const uint64_t q = f32x2_fma(f32x2_fma(q0, ns2, w), r2, q0);
+                const uint64_t t = f32x2_add(f32x2_add(q, z2), m2);
+                uint32_t p2 = __byte_perm((uint32_t)t, (uint32_t)(t >> 32), 0x5410);
+                p2 = __vmins2(__vmaxs2(p2, 0u), 0x000F000Fu);
+                b[i] = p2 | (p2 >> 12);  // byte 0: the pair's first code | second << 4
+            }
+            code[j] = __byte_perm(__byte_perm(b[0], b[1], 0x0040), __byte_perm(b[2], b[3], 0x0040), 0x5410);
+        }
+    } else {
+        z = round_bf16(__fadd_rn(rintf(__fdiv_rn(-mn, s)), 0.0f));
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            const float w = __uint_as_float(e ? (word & 0xffff0000u) : (word << 16));
-            if (fast) {
-                const float wc = fminf(fmaxf(w, -top), top);
-                float t = __fmul_rn(wc, r);
-                t = __fmaf_rn(__fmaf_rn(-t, s, wc), r, t);
-                t = __fmaf_rn(__fmaf_rn(-t, s, wc), r, t);
-                q[e] = copysignf(t, w);  // the corrections turn -0 into +0
-            } else {
-                q[e] = __fdiv_rn(w, s);
+        for (int j = 0; j < 2; ++j) {
+            code[j] = 0u - kRintBase * 0x11111111u;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const uint64_t p = pair_of(raw, 4 * j + (i >> 1));
+                const float t = __fadd_rn(__fdiv_rn((i & 1) ? hi_of(p) : lo_of(p), s), z);
+                code[j] += rint_bits(fminf(fmaxf(t, 0.0f), 15.0f)) << (4 * i);
             }
         }
-        uint16_t h;
-        asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(h) : "f"(q[1]), "f"(q[0]));
-        c[i] = h;
     }
-    return make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
+    return make_uint2(code[0], code[1]);
 }
 
-// Vector index j runs over (token, K or V, head): a token's heads are adjacent, so are their 16-lane groups.
+__device__ __forceinline__ uint32_t e4m3x2(float lo, float hi)
+{
+    uint16_t h;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(h) : "f"(hi), "f"(lo));
+    return h;
+}
+
+// This lane's 16 E4M3 codes against the tensor's scale s.
+__device__ __forceinline__ uint4 fp8_codes(const uint4 raw[2], float s)
+{
+    uint32_t m2 = raw[0].x & 0x7FFF7FFFu;
+#pragma unroll
+    for (int i = 1; i < 8; ++i) m2 = bf16x2_max(m2, word_of(raw[i >> 2], i & 3) & 0x7FFF7FFFu);
+    const float maxabs = fmaxf(__uint_as_float(m2 << 16), __uint_as_float(m2 & 0xffff0000u));
+    uint32_t c[8];
+    if (quotients_by_reciprocal(s, maxabs)) {
+        const float r = __frcp_rn(s);
+        const uint64_t r2 = f32x2_bits(r, r), ns2 = f32x2_bits(-s, -s);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const uint64_t w = pair_of(raw, i);
+            uint64_t q = f32x2_mul(w, r2);
+            q = f32x2_fma(f32x2_fma(q, ns2, w), r2, q);
+            q = f32x2_fma(f32x2_fma(q, ns2, w), r2, q);
+            c[i] = e4m3x2(lo_of(q), hi_of(q));
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const uint64_t w = pair_of(raw, i);
+            c[i] = e4m3x2(__fdiv_rn(lo_of(w), s), __fdiv_rn(hi_of(w), s));
+        }
+    }
+    uint32_t word[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        // a code's sign is its value's (s > 0; the corrections turn -0 into +0)
+        const uint32_t sign = __byte_perm(word_of(raw[i >> 1], (2 * i) & 3), word_of(raw[i >> 1], (2 * i + 1) & 3), 0x7531);
+        word[i] = __byte_perm(c[2 * i], c[2 * i + 1], 0x5410) | (sign & 0x80808080u);
+    }
+    return make_uint4(word[0], word[1], word[2], word[3]);
+}
+
+// Vector index j runs over (token, K or V, head): a token's heads are adjacent, so are their groups of lanes.
 template <bool FP8>
 __global__ void __launch_bounds__(kThreads)
 kv_store_kernel(const StoreArgs p)
 {
-    constexpr int kGroups = kThreads / kLanes;
-    const int l = threadIdx.x % kLanes, g = threadIdx.x / kLanes;
-    const int64_t vectors = p.M * 2 * p.H;
-    float s8[2] = {0.0f, 0.0f}, r8[2] = {0.0f, 0.0f};
-    bool fast8[2] = {false, false};
-    if (FP8) {
-        s8[0] = *p.k8s;
-        s8[1] = *p.v8s;
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            fast8[e] = s8[e] >= 0x1p-100f && s8[e] <= 0x1p100f;
-            r8[e] = __frcp_rn(s8[e]);
-        }
-    }
-    const int64_t j0 = (int64_t)blockIdx.x * (kGroups * kUnroll) + g;
-    uint4 raw[kUnroll];
+    const unsigned l = threadIdx.x % kLanes, g = threadIdx.x / kLanes, H = (unsigned)p.H;
+    const unsigned vectors = (unsigned)p.M * 2u * H;
+    const unsigned j0 = blockIdx.x * (kGroups * kUnroll) + g;
+    uint4 raw[kUnroll][2];
     int64_t slot[kUnroll], row[kUnroll];
     bool is_v[kUnroll];
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
-        const int64_t j = j0 + u * kGroups;
+        const unsigned j = j0 + u * kGroups;
         slot[u] = -1;
-        raw[u] = make_uint4(0u, 0u, 0u, 0u);
+        raw[u][0] = raw[u][1] = make_uint4(0u, 0u, 0u, 0u);
         row[u] = 0;
         is_v[u] = false;
         if (j < vectors) {
-            const int64_t m = j / (2 * p.H);
-            const int rest = (int)(j - m * 2 * p.H);
-            is_v[u] = rest >= p.H;
-            const int h = is_v[u] ? rest - p.H : rest;
-            slot[u] = p.slots[m];
+            const unsigned m = j / (2u * H), rest = j - m * 2u * H;
+            is_v[u] = rest >= H;
+            const unsigned h = is_v[u] ? rest - H : rest;
+            slot[u] = __ldg(p.slots + m);
             if (slot[u] >= p.S) slot[u] = -1;
-            raw[u] = ld_stream_v4((is_v[u] ? p.v + m * p.ldv : p.k + m * p.ldk) + h * kD + l * 8);
-            row[u] = slot[u] * p.H + h;
+            const uint16_t *src = (is_v[u] ? p.v + m * p.ldv : p.k + m * p.ldk) + h * kD + l * 16;
+            raw[u][0] = ld_stream_v4(src);
+            raw[u][1] = ld_stream_v4(src + 8);
+            row[u] = slot[u] * H + h;
         }
     }
+    const float ks = FP8 ? __ldg(p.k8s) : 0.0f, vs = FP8 ? __ldg(p.v8s) : 0.0f;
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
         if (FP8) {
-            const uint2 c = is_v[u] ? fp8_codes(raw[u], s8[1], r8[1], fast8[1]) : fp8_codes(raw[u], s8[0], r8[0], fast8[0]);
-            if (slot[u] >= 0) *reinterpret_cast<uint2 *>((is_v[u] ? p.vc : p.kc) + row[u] * kD + l * 8) = c;
+            const uint4 c = fp8_codes(raw[u], is_v[u] ? vs : ks);
+            if (slot[u] >= 0) *reinterpret_cast<uint4 *>((is_v[u] ? p.vc : p.kc) + row[u] * kD + l * 16) = c;
         } else {
             float s, z;
-            const uint32_t c = int4_block(raw[u], s, z);
+            const uint2 c = int4_block(raw[u], s, z);
             if (slot[u] >= 0) {
-                *reinterpret_cast<uint32_t *>((is_v[u] ? p.vc : p.kc) + row[u] * (kD / 2) + l * 4) = c;
+                *reinterpret_cast<uint2 *>((is_v[u] ? p.vc : p.kc) + row[u] * (kD / 2) + l * 8) = c;
                 if (l == 0) {
                     (is_v[u] ? p.vs : p.ks)[row[u]] = f32_to_bf16(s);
                     (is_v[u] ? p.vz : p.kz)[row[u]] = f32_to_bf16(z);
@@ -165,7 +210,7 @@ void launch_kv_store(bool fp8, const uint16_t *k, int64_t ldk, const uint16_t *v
                      uint8_t *vc, uint16_t *vs, uint16_t *vz, const float *v8s, cudaStream_t st)
 {
     const StoreArgs a{k, v, ldk, ldv, slots, M, S, (int)H, kc, vc, ks, kz, vs, vz, k8s, v8s};
-    const int64_t per = (int64_t)(kThreads / kLanes) * kUnroll;
+    const int64_t per = (int64_t)kGroups * kUnroll;
     const unsigned grid = (unsigned)((M * 2 * H + per - 1) / per);
     if (fp8) kv_store_kernel<true><<<grid, kThreads, 0, st>>>(a);
     else kv_store_kernel<false><<<grid, kThreads, 0, st>>>(a);

@@ -560,8 +560,8 @@ int wq_qk_norm_rope(const uint16_t *q, int64_t ldq, const uint16_t *k, int64_t l
  *   cache     as described under wq_decode_attention_int4 / _fp8; vectors of
  *             no slot are left as they are
  *   k_scale, v_scale  one positive binary32 value each, on the device
- * Requirements: M, S, H >= 1; D == 128 (WQ_ERR_UNSUPPORTED otherwise); ldk,
- * ldv >= H * D and multiples of 8; rows and cache 16-byte aligned, slots
+ * Requirements: M, S, H >= 1, M * H < 2^30; D == 128 (WQ_ERR_UNSUPPORTED
+ * otherwise); ldk, ldv >= H * D and multiples of 8; rows and cache 16-byte aligned, slots
  * 8-byte, fp8 scales 4-byte; no part of the cache overlaps an input or another
  * part.
  */

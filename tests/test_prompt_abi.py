@@ -96,8 +96,8 @@ def _store(L, fp8=False, **kw):
 @pytest.mark.parametrize("kw,code", [
     (dict(k=None), ARG), (dict(v=None), ARG), (dict(slots=None), ARG), (dict(kc=None), ARG), (dict(ks=None), ARG),
     (dict(vs=None), ARG), (dict(M=0), ARG), (dict(S=0), ARG), (dict(H=-2), ARG), (dict(D=64), UNSUPPORTED),
-    (dict(ldk=248), SHAPE), (dict(ldv=128), SHAPE), (dict(ldk=260), ALIGN), (dict(k=X + 8), ALIGN),
-    (dict(slots=S + 4), ALIGN), (dict(kc=W + 8), ALIGN), (dict(ks=Y + 2), ALIGN),
+    (dict(ldk=248), SHAPE), (dict(ldv=128), SHAPE), (dict(M=1 << 29), SHAPE), (dict(S=1 << 41), SHAPE),
+    (dict(ldk=260), ALIGN), (dict(k=X + 8), ALIGN), (dict(slots=S + 4), ALIGN), (dict(kc=W + 8), ALIGN), (dict(ks=Y + 2), ALIGN),
     (dict(kc=X + 64), ARG), (dict(vc=W + 4096), ARG), (dict(vc=S), ARG), (dict(vc=Q), ARG),
 ])
 def test_kv_store_rejects(L, fp8, kw, code):
