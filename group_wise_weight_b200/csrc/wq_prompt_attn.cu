@@ -1,5 +1,5 @@
 // wq_prompt_attn.cu -- causal attention over whole prompts packed one after
-// another, with grouped query heads.
+// another, with grouped query heads, on the 5th-generation tensor cores.
 //
 // Scaled dot-product attention (Vaswani et al. 2017, section 3.2.1) of token
 // t of a sequence, query head j, over the tokens u <= t of the same sequence
@@ -10,43 +10,100 @@
 //
 // One pass over the keys with the running maximum m and sum l of the softmax
 // (Milakov and Gimelshein 2018): when m grows, l and the output accumulator
-// are scaled by e^(m_old - m_new).  Scores, m, l and the accumulator are
-// binary32; p is rounded to bf16 as the second product's operand (a rounding
-// of at most 2^-8 of each term), while l sums the
-// unrounded p.
+// are scaled by e^(m_old - m_new).  Scaling is put off until m would grow by
+// more than a factor of 2^8 in p (p, l and the accumulator then carry the old
+// m, exactly; binary32 has room for 2^8 L), which leaves it to the first few
+// blocks of most rows.  Scores, m, l and the accumulator are binary32; p is
+// rounded to bf16 as the second product's operand (at most 2^-8 of each
+// term), while l sums the unrounded p.
 //
 // The r = Hq / H query heads of a KV head share its keys and values: a tile's
-// rows are (token, head) pairs, token-major, so a tile of 64 rows covers
-// 64 / r tokens and reads each key once for all r heads.
+// 128 rows are (token, head) pairs, token-major, so it covers 128 / r tokens
+// and short sequences still fill it.  A work item is two such tiles
+// (consecutive tokens) of one KV head; a persistent CTA per SM takes items,
+// the longest first.
+//
+// Per block of 128 keys and tile: S = Q K^T (both operands K-major in shared
+// memory, loaded by TMA with the 128-byte swizzle) into 128 columns of tensor
+// memory; a warpgroup, one row per thread, turns S into P in place (bf16,
+// the first 64 columns); O += P V with P from tensor memory and V from shared
+// memory as it lies there (key rows, so the operand is MN-major).  The two
+// tiles are half a period apart: while one's warpgroup is in its softmax the
+// tensor core works on the other.  The block's two products take 1,024 cycles
+// of the tensor core per tile and its 16,384 exponentials as many of the
+// special-function units, so both are at their limits together.
+//
+// Roles (320 threads): warps 0-3 and 4-7 the two softmax warpgroups, warp 8
+// the copies (Q of the next item as soon as its tile is free, a ring of K and
+// V blocks), warp 9 the MMAs.  Keys past a tile's last visible one are left
+// out of both products in steps of 16; inside the step their p is 0, and V
+// rows past the sequence's end are zeroed in shared memory, so what lies
+// behind a sequence never enters a sum.  Every barrier wait is bounded.
 #include <algorithm>
+#include <atomic>
 
-#include "wq_common.cuh"
 #include "wq_internal.h"
+#include "wq_sm100.cuh"
 
 namespace wq {
 
 namespace {
 
-constexpr int kRows = 64;   // (token, head) rows per CTA, 16 per warp
-constexpr int kKeys = 64;   // keys per step
-constexpr int kThreads = 128;
+constexpr int kRows = 128;      // (token, head) rows per tile
+constexpr int kKeys = 128;      // keys per block
+constexpr int kThreads = 320;
+constexpr int kLoadWarp = 8, kMmaWarp = 9;
+constexpr uint32_t kTmemCols = 512;
+constexpr float kSlack = 8.0f;  // log2 of the growth of p that is let pass before m moves
+
+template <int D>
+struct Cfg {
+    static constexpr int kCols = D / 64;               // 128-byte column blocks of a row
+    static constexpr int kBlkBytes = kRows * 128;      // one column block of 128 rows
+    static constexpr int kTileBytes = kCols * kBlkBytes;
+    static constexpr int kStages = D == 128 ? 5 : 8;   // K and V blocks in the ring
+    static constexpr int kRing = 2 * kTileBytes;       // after the two Q tiles
+    static constexpr int kBarOff = kRing + kStages * kTileBytes;
+    static constexpr int kBytes = kBarOff + 512;
+};
 
 struct PromptArgs {
-    const uint16_t *q, *k, *v;
-    int64_t ldq, ldk, ldv, ldo, M;
     const int32_t *starts;
+    int64_t M, ldo;
     int B, H, r, tpt;  // tokens per tile
     float scale_log2;  // log2(e) / sqrt(D)
     uint16_t *o;
+    int *status;
 };
 
-// Tile `t` of the packed batch: its sequence's first row and length, and the tile's first token in it.  Whole
-// warp; false when there is no such tile.  Bounds outside [0, M] are clamped, a sequence that ends before it
-// begins is empty.
-__device__ __forceinline__ bool locate_tile(const PromptArgs &p, int64_t t, int64_t &row0, int &len, int &tok0)
+// One work item: tiles at tokens tok0 and tok0 + tpt of the sequence at row0, KV head h.
+struct Item {
+    int64_t row0;
+    int len, tok0, h, valid;
+    // keys seen by some row of tile x, and its blocks (0: no such tile)
+    __device__ __forceinline__ int last(int x, int tpt) const { return std::min(len, tok0 + (x + 1) * tpt); }
+    __device__ __forceinline__ int blocks(int x, int tpt) const
+    {
+        return tok0 + x * tpt < len ? (last(x, tpt) + kKeys - 1) / kKeys : 0;
+    }
+};
+
+struct Bars {
+    uint64_t kv_full[8], kv_empty[8], q_full[2], q_empty[2], s_full[2], p_full[2], pv_done[2], item_full[2], item_empty[2], done;
+    Item items[2];
+    int abort, pad;
+    uint32_t tmem;
+};
+static_assert(sizeof(Bars) <= 512, "the barrier area");
+
+// Pairs of tiles of the packed batch in order; the one with index `t`: its sequence's first row and length and its
+// first token.  Whole warp; returns the number of pairs seen up to and including its sequence's, and sets `found`.
+// Bounds outside [0, M] are clamped, a sequence that ends before it begins is empty.
+__device__ __forceinline__ bool locate(const PromptArgs &p, int64_t t, Item &it, int64_t &all)
 {
-    const int lane = threadIdx.x & 31;
+    const int lane = threadIdx.x & 31, span = 2 * p.tpt;
     int64_t before = 0;
+    bool found = false;
     for (int b0 = 0; b0 < p.B; b0 += 32) {
         const int b = b0 + lane;
         int64_t s = 0, e = 0;
@@ -54,153 +111,406 @@ __device__ __forceinline__ bool locate_tile(const PromptArgs &p, int64_t t, int6
             s = std::min<int64_t>(std::max<int64_t>(p.starts[b], 0), p.M);
             e = std::min<int64_t>(std::max<int64_t>(p.starts[b + 1], s), p.M);
         }
-        const int64_t n = (e - s + p.tpt - 1) / p.tpt;
+        const int64_t n = (e - s + span - 1) / span;
         int64_t upto = n;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const int64_t x = __shfl_up_sync(0xffffffffu, upto, o);
             if (lane >= o) upto += x;
         }
-        const unsigned hit = __ballot_sync(0xffffffffu, before + upto > t);
+        const unsigned hit = __ballot_sync(0xffffffffu, t >= 0 && before + upto > t);
         if (hit) {
             const int src = __ffs(hit) - 1;
-            row0 = __shfl_sync(0xffffffffu, s, src);
-            len = (int)__shfl_sync(0xffffffffu, e - s, src);
-            tok0 = (int)(t - before - __shfl_sync(0xffffffffu, upto - n, src)) * p.tpt;
-            return true;
+            it.row0 = __shfl_sync(0xffffffffu, s, src);
+            it.len = (int)__shfl_sync(0xffffffffu, e - s, src);
+            it.tok0 = (int)(t - before - __shfl_sync(0xffffffffu, upto - n, src)) * span;
+            found = true;
+            break;
         }
         before += __shfl_sync(0xffffffffu, upto, 31);
     }
-    return false;
+    all = before;  // the total only when nothing was found
+    return found;
 }
 
-__device__ __forceinline__ void mma_bf16(float c[4], const uint32_t a[4], uint32_t b0, uint32_t b1)
+// 2^x, the hardware's approximation (denormal results flushed).
+__device__ __forceinline__ float ex2(float x)
 {
-    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 "
-        "{%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
-        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+struct Wait {
+    int *status;
+    volatile int *abort;
+    __device__ __forceinline__ bool operator()(uint64_t *bar, uint32_t parity) const
+    {
+        return mbar_wait_fast(bar, parity, status, abort);
+    }
+};
+
+// Instruction descriptor: bf16 operands, f32 accumulator; PV reads V with its keys along K in rows of D (MN-major).
+__device__ __forceinline__ uint32_t idesc_qk(int n) { return idesc_bf16_f32(kRows, n); }
+__host__ __device__ constexpr uint32_t idesc_pv(int d) { return idesc_bf16_f32(kRows, d) | (1u << 16); }
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+prompt_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
+                   const __grid_constant__ CUtensorMap vmap, const PromptArgs p)
+{
+    using C = Cfg<D>;
+    constexpr uint32_t S = (uint32_t)C::kStages;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
+    Bars &b = *reinterpret_cast<Bars *>(smem + C::kBarOff);
+    const int tid = threadIdx.x, wid = tid >> 5, lane = tid & 31;
+    const Wait wait{p.status, &b.abort};
+
+    if (tid == 0) {
+        for (uint32_t i = 0; i < S; ++i) {
+            mbar_init(&b.kv_full[i], 1);
+            mbar_init(&b.kv_empty[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&b.q_full[i], 1);
+            mbar_init(&b.q_empty[i], 1);
+            mbar_init(&b.s_full[i], 1);
+            mbar_init(&b.p_full[i], 4);
+            mbar_init(&b.pv_done[i], 1);
+            mbar_init(&b.item_full[i], 1);
+            mbar_init(&b.item_empty[i], 9);  // 8 softmax warps and the MMA warp
+        }
+        mbar_init(&b.done, 1);
+        b.abort = 0;
+        fence_mbar_init();
+    }
+    if (wid == kMmaWarp) tmem_alloc(&b.tmem, kTmemCols);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = b.tmem;  // S of tile x at 128 x, O of tile x at 256 + D x
+
+    if (wid == kLoadWarp) {
+        // ------------------------------ items and copies ------------------------------
+        Item it{};
+        int64_t pairs;
+        locate(p, -1, it, pairs);
+        const int64_t total = pairs * p.H;
+        uint32_t slot = 0, phase = 0, loads = 0, nitem = 0, qn[2] = {0, 0};
+        bool ok = true;
+        for (int64_t i = blockIdx.x;; i += gridDim.x) {
+            const uint32_t s = nitem & 1u;
+            if (nitem >= 2 && !wait(&b.item_empty[s], ((nitem >> 1) - 1) & 1u)) { ok = false; break; }
+            it.valid = i < total;
+            if (it.valid) {
+                const int64_t pair = pairs - 1 - i / p.H;  // the last pairs of the sequences first: the longest
+                int64_t unused;
+                locate(p, pair, it, unused);
+                it.h = (int)(i % p.H);
+            }
+            if (lane == 0) {
+                b.items[s] = it;
+                mbar_arrive(&b.item_full[s]);
+            }
+            __syncwarp();
+            ++nitem;
+            if (!it.valid) break;
+            const int n0 = it.blocks(0, p.tpt), n1 = it.blocks(1, p.tpt), n = std::max(n0, n1);
+            auto load_q = [&](int x) {
+                if (qn[x] > 0 && !wait(&b.q_empty[x], (qn[x] - 1) & 1u)) return false;
+                if (lane == 0) {
+                    mbar_arrive_expect_tx(&b.q_full[x], (uint32_t)(C::kCols * p.r * p.tpt * 128));
+                    for (int c = 0; c < C::kCols; ++c)
+                        tma_load_3d(smem + x * C::kTileBytes + c * C::kBlkBytes, &qmap, &b.q_full[x], c * 64,
+                                    it.h * p.r, (int)it.row0 + it.tok0 + x * p.tpt);
+                }
+                ++qn[x];
+                return true;
+            };
+            auto load_kv = [&](const CUtensorMap *map, int j) {
+                if (loads >= S && !wait(&b.kv_empty[slot], phase ^ 1u)) return false;
+                if (lane == 0) {
+                    mbar_arrive_expect_tx(&b.kv_full[slot], (uint32_t)C::kTileBytes);
+                    for (int c = 0; c < C::kCols; ++c)
+                        tma_load_3d(smem + C::kRing + slot * C::kTileBytes + c * C::kBlkBytes, map, &b.kv_full[slot],
+                                    c * 64, it.h, (int)it.row0 + j * kKeys);
+                }
+                ++loads;
+                if (++slot == S) { slot = 0; phase ^= 1u; }
+                return true;
+            };
+            ok = load_q(0) && load_kv(&kmap, 0) && (n1 == 0 || load_q(1)) && load_kv(&vmap, 0);
+            for (int j = 1; ok && j < n; ++j) ok = load_kv(&kmap, j) && load_kv(&vmap, j);
+            if (!ok) break;
+        }
+        if (lane == 0) {
+            // every issued copy must land before the CTA may exit (bounded, ignoring abort)
+            auto drain = [&](uint64_t *bar, uint32_t parity) {
+                const uint64_t t0 = global_ns();
+                while (!mbar_try_wait(bar, parity))
+                    if (global_ns() - t0 > kWaitLimitNs) { record_timeout(p.status); return; }
+            };
+            for (uint32_t j = loads > S ? loads - S : 0; j < loads; ++j) drain(&b.kv_full[j % S], (j / S) & 1u);
+            for (int x = 0; x < 2; ++x)
+                if (qn[x] > 0) drain(&b.q_full[x], (qn[x] - 1) & 1u);
+        }
+        (void)ok;
+    } else if (wid == kMmaWarp) {
+        // ------------------------------ MMAs (lane 0 issues) ------------------------------
+        uint32_t slot = 0, phase = 0, nitem = 0, qn[2] = {0, 0}, sn[2] = {0, 0}, pvn[2] = {0, 0};
+        const uint32_t base = smem_u32(smem);
+        bool ok = true;
+        auto next_slot = [&]() {
+            if (++slot == S) { slot = 0; phase ^= 1u; }
+        };
+        while (ok) {
+            const uint32_t is = nitem & 1u;
+            if (!wait(&b.item_full[is], (nitem >> 1) & 1u)) break;
+            const Item it = b.items[is];
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&b.item_empty[is]);
+            ++nitem;
+            if (!it.valid) break;
+            const int nb[2] = {it.blocks(0, p.tpt), it.blocks(1, p.tpt)}, n = std::max(nb[0], nb[1]);
+            // S of tile x and block j (its K in ring slot `ks`): S's columns hold the P of the block before, which its
+            // product must have read
+            auto qk = [&](int x, int j, uint32_t ks) {
+                if (pvn[x] > 0 && !wait(&b.pv_done[x], (pvn[x] - 1) & 1u)) return false;
+                tc_fence_after();
+                if (lane == 0) {
+                    const int keys = min(kKeys, it.last(x, p.tpt) - j * kKeys);
+                    const uint32_t idesc = idesc_qk((keys + 15) & ~15);
+                    const uint32_t q = base + x * C::kTileBytes, k = base + C::kRing + ks * C::kTileBytes;
+#pragma unroll
+                    for (int e = 0; e < D / 16; ++e) {
+                        const uint32_t off = (uint32_t)(e / 4 * C::kBlkBytes + e % 4 * 32);
+                        tc_mma_ss(tmem + 128u * x, smem_desc(q + off, 16, 1024, 2), smem_desc(k + off, 16, 1024, 2), idesc, e > 0);
+                    }
+                    tc_commit(&b.s_full[x]);
+                    if (j + 1 == nb[x]) tc_commit(&b.q_empty[x]);
+                }
+                __syncwarp();
+                ++sn[x];
+                return true;
+            };
+            auto pv = [&](int x, int j, uint32_t vs) {
+                if (!wait(&b.p_full[x], pvn[x] & 1u)) return false;
+                tc_fence_after();
+                if (lane == 0) {
+                    const int keys = min(kKeys, it.last(x, p.tpt) - j * kKeys);
+                    const uint32_t v = base + C::kRing + vs * C::kTileBytes;
+#pragma unroll
+                    for (int e = 0; e < kKeys / 16; ++e)
+                        if (e * 16 < keys)
+                            tc_mma_ts(tmem + 256u + (uint32_t)D * x, tmem + 128u * x + 8u * e,
+                                      smem_desc(v + 2048u * e, C::kBlkBytes, 1024, 2), idesc_pv(D), (j > 0 || e > 0) ? 1u : 0u);
+                    tc_commit(&b.pv_done[x]);
+                }
+                __syncwarp();
+                ++pvn[x];
+                return true;
+            };
+            auto release = [&](uint32_t s) {
+                if (lane == 0) tc_commit(&b.kv_empty[s]);
+                __syncwarp();
+            };
+            // Q and the first K
+            uint32_t ks = slot;
+            ok = wait(&b.q_full[0], qn[0]++ & 1u) && wait(&b.kv_full[slot], phase) && qk(0, 0, ks);
+            next_slot();
+            if (ok && nb[1] > 0) ok = wait(&b.q_full[1], qn[1]++ & 1u) && qk(1, 0, ks);
+            if (!ok) break;
+            release(ks);
+            for (int j = 0; ok && j < n; ++j) {
+                const uint32_t vs = slot;
+                ok = wait(&b.kv_full[vs], phase);
+                if (!ok) break;
+                next_slot();
+                const int in_seq = it.len - j * kKeys;  // V rows from here on are no part of the sequence
+                if (in_seq < kKeys && (in_seq & 15)) {
+                    const int rows = 16 - (in_seq & 15);
+                    for (int i = lane; i < rows * 8 * C::kCols; i += 32) {
+                        const int c = i / (rows * 8), w = i % (rows * 8);
+                        *reinterpret_cast<uint4 *>(smem + C::kRing + vs * C::kTileBytes + c * C::kBlkBytes + in_seq * 128 + w * 16) =
+                            make_uint4(0u, 0u, 0u, 0u);
+                    }
+                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                    __syncwarp();
+                }
+                const uint32_t k1 = slot;
+                bool have_k = false;
+                for (int x = 0; ok && x < 2; ++x) {
+                    if (j < nb[x]) ok = pv(x, j, vs);
+                    if (ok && j + 1 < nb[x]) {
+                        if (!have_k) ok = wait(&b.kv_full[k1], phase);
+                        have_k = true;
+                        ok = ok && qk(x, j + 1, k1);
+                    }
+                }
+                if (!ok) break;
+                release(vs);
+                if (j + 1 < n) {
+                    next_slot();
+                    release(k1);
+                }
+            }
+        }
+        if (lane == 0) {
+            tc_commit(&b.done);
+            const uint64_t t0 = global_ns();
+            while (!mbar_try_wait(&b.done, 0))  // every MMA must complete before tensor memory is released
+                if (global_ns() - t0 > kWaitLimitNs) { record_timeout(p.status); break; }
+        }
+        __syncwarp();
+    } else {
+        // ------------------------------ softmax and output, one row per thread ------------------------------
+        const int x = wid >> 2, row = tid & 127;
+        const uint32_t lane_bits = (uint32_t)((wid & 3) * 32) << 16;
+        const uint32_t s_addr = tmem + lane_bits + 128u * x, o_addr = tmem + lane_bits + 256u + (uint32_t)D * x;
+        const int row_tok = row / p.r, row_head = row - row_tok * p.r;
+        uint32_t nitem = 0, blocks_done = 0;
+        bool ok = true;
+        while (ok) {
+            const uint32_t is = nitem & 1u;
+            if (!wait(&b.item_full[is], (nitem >> 1) & 1u)) break;
+            const Item it = b.items[is];
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&b.item_empty[is]);
+            ++nitem;
+            if (!it.valid) break;
+            const int nb = it.blocks(x, p.tpt), last = it.last(x, p.tpt), tile_tok = it.tok0 + x * p.tpt;
+            const int tok = tile_tok + row_tok;
+            float m = -INFINITY, l = 0.0f;
+            for (int j = 0; j < nb; ++j) {
+                if (!wait(&b.s_full[x], blocks_done & 1u)) { ok = false; break; }
+                tc_fence_after();
+                const int u0 = j * kKeys, keys = min(kKeys, last - u0);
+                uint32_t v[kKeys];
+#pragma unroll
+                for (int c = 0; c < kKeys / 32; ++c)
+                    if (c * 32 < keys) tmem_ld32(s_addr + 32u * c, v + 32 * c);
+                tmem_wait_ld();
+                const bool edge = u0 + kKeys > tile_tok + 1;  // some row does not see every key of the block
+                if (edge) {
+#pragma unroll
+                    for (int c = 0; c < kKeys; ++c)
+                        if (c >= keys || c > tok - u0) v[c] = 0xff800000u;
+                }
+                float top = m;
+#pragma unroll
+                for (int c = 0; c < kKeys; c += 2)
+                    top = fmaxf(top, fmaxf(__uint_as_float(v[c]), __uint_as_float(v[c + 1])));
+                const bool grow = (top - m) * p.scale_log2 > kSlack;
+                if (__any_sync(0xffffffffu, grow)) {
+                    const float keep = ex2((m - top) * p.scale_log2);
+                    m = top;
+                    l *= keep;
+                    if (j > 0) {
+                        // the product of the block before has completed: S was issued after it
+#pragma unroll 1
+                        for (int c = 0; c < D; c += 32) {
+                            uint32_t w[32];
+                            tmem_ld32(o_addr + (uint32_t)c, w);
+                            tmem_wait_ld();
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) w[e] = __float_as_uint(__uint_as_float(w[e]) * keep);
+                            tmem_st32(o_addr + (uint32_t)c, w);
+                        }
+                    }
+                }
+                const float shift = -m * p.scale_log2;
+                const f32x2 sc{p.scale_log2, p.scale_log2}, sh{shift, shift};
+                f32x2 sum[2] = {{0.0f, 0.0f}, {0.0f, 0.0f}};
+#pragma unroll
+                for (int c = 0; c < kKeys / 32; ++c) {
+                    if (c * 32 < keys) {
+                        uint32_t w[16];
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) {
+                            const f32x2 s2{__uint_as_float(v[32 * c + 2 * e]), __uint_as_float(v[32 * c + 2 * e + 1])};
+                            const f32x2 y = fma2_pairs(s2, sc, sh);
+                            const f32x2 q{ex2(y.x), ex2(y.y)};
+                            sum[e & 1] = add2(sum[e & 1], q);
+                            w[e] = pack_bf16x2(q.x, q.y);
+                        }
+                        tmem_st16(s_addr + 16u * c, w);
+                    }
+                }
+                const f32x2 both = add2(sum[0], sum[1]);
+                l += both.x + both.y;
+                tmem_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&b.p_full[x]);
+                ++blocks_done;
+            }
+            if (!ok) break;
+            if (nb == 0) continue;
+            if (!wait(&b.pv_done[x], (blocks_done - 1) & 1u)) break;
+            tc_fence_after();
+            const float inv = 1.0f / l;
+            const bool live = row < p.tpt * p.r && tok < it.len;
+            uint16_t *dst = p.o + (it.row0 + tok) * p.ldo + (it.h * p.r + row_head) * D;
+#pragma unroll 1
+            for (int c = 0; c < D; c += 32) {
+                uint32_t w[32];
+                tmem_ld32(o_addr + (uint32_t)c, w);
+                tmem_wait_ld();
+                if (live) {
+#pragma unroll
+                    for (int e = 0; e < 32; e += 8) {
+                        uint32_t h[4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            h[i] = pack_bf16x2(__uint_as_float(w[e + 2 * i]) * inv, __uint_as_float(w[e + 2 * i + 1]) * inv);
+                        *reinterpret_cast<uint4 *>(dst + c + e) = make_uint4(h[0], h[1], h[2], h[3]);
+                    }
+                }
+            }
+            tc_fence_before();  // the next item's first product into O follows this warpgroup's next P
+        }
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (wid == kMmaWarp) tmem_dealloc(tmem, kTmemCols);
+}
+
+// SMs of the current device; the kernels' shared-memory limit is raised on its first use there.
+int sms_of_device()
+{
+    static std::atomic<int> sms_of[128] = {};
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 128) return 0;
+    int sms = sms_of[dev].load(std::memory_order_acquire);
+    if (sms == 0) {
+        if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
+        cudaFuncSetAttribute(prompt_attn_kernel<64>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<64>::kBytes + 1024);
+        cudaFuncSetAttribute(prompt_attn_kernel<128>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<128>::kBytes + 1024);
+        sms_of[dev].store(sms, std::memory_order_release);
+    }
+    return sms;
 }
 
 template <int D>
-__global__ void __launch_bounds__(kThreads)
-prompt_attn_kernel(const PromptArgs p)
+int run(const uint16_t *q, int64_t ldq, const uint16_t *k, int64_t ldk, const uint16_t *v, int64_t ldv, int64_t Hq,
+        const PromptArgs &a, cudaStream_t st)
 {
-    constexpr int kPitch = D + 8;  // halves; the pad keeps fragment loads off one bank
-    extern __shared__ __align__(16) uint16_t sm[];
-    uint16_t *ks = sm, *vs = sm + kKeys * kPitch;
-    const int tid = threadIdx.x, wid = tid >> 5, lane = tid & 31, gr = lane >> 2, gc = lane & 3;
-    const int h = blockIdx.y;
-    int64_t row0;
-    int len, tok0;
-    if (!locate_tile(p, blockIdx.x, row0, len, tok0)) return;
-
-    // this lane's two rows: tile rows 16 wid + gr and + 8
-    int tok[2], head[2];
-    bool live[2];
-    uint32_t qf[D / 16][4];
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-        const int i = wid * 16 + gr + 8 * e;
-        tok[e] = tok0 + i / p.r;
-        head[e] = h * p.r + i % p.r;
-        live[e] = i < p.tpt * p.r && tok[e] < len;
-        const uint16_t *src = p.q + (row0 + (live[e] ? tok[e] : 0)) * p.ldq + head[e] * D;
-#pragma unroll
-        for (int c = 0; c < D / 16; ++c) {
-            qf[c][e] = *reinterpret_cast<const uint32_t *>(src + c * 16 + gc * 2);
-            qf[c][e + 2] = *reinterpret_cast<const uint32_t *>(src + c * 16 + 8 + gc * 2);
-        }
-    }
-    float o[D / 8][4], mx[2] = {-INFINITY, -INFINITY}, sum[2] = {0.0f, 0.0f};
-#pragma unroll
-    for (int i = 0; i < D / 8; ++i)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) o[i][e] = 0.0f;
-
-    const int last = std::min(len, tok0 + p.tpt);  // keys 0 .. last - 1 are seen by some row
-    for (int u0 = 0; u0 < last; u0 += kKeys) {
-        __syncthreads();
-        for (int i = tid; i < kKeys * (D / 8); i += kThreads) {
-            const int u = i / (D / 8), c = i % (D / 8) * 8;
-            uint4 kv = make_uint4(0u, 0u, 0u, 0u), vv = kv;
-            if (u0 + u < last) {
-                kv = *reinterpret_cast<const uint4 *>(p.k + (row0 + u0 + u) * p.ldk + h * D + c);
-                vv = *reinterpret_cast<const uint4 *>(p.v + (row0 + u0 + u) * p.ldv + h * D + c);
-            }
-            *reinterpret_cast<uint4 *>(ks + u * kPitch + c) = kv;
-            *reinterpret_cast<uint4 *>(vs + u * kPitch + c) = vv;
-        }
-        __syncthreads();
-        float s[kKeys / 8][4];
-#pragma unroll
-        for (int n = 0; n < kKeys / 8; ++n) {
-#pragma unroll
-            for (int e = 0; e < 4; ++e) s[n][e] = 0.0f;
-#pragma unroll
-            for (int c = 0; c < D / 16; ++c) {
-                const uint16_t *b = ks + (n * 8 + gr) * kPitch + c * 16 + gc * 2;
-                mma_bf16(s[n], qf[c], *reinterpret_cast<const uint32_t *>(b), *reinterpret_cast<const uint32_t *>(b + 8));
-            }
-        }
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            float top = mx[e];
-#pragma unroll
-            for (int n = 0; n < kKeys / 8; ++n)
-#pragma unroll
-                for (int x = 0; x < 2; ++x) {
-                    const int u = u0 + n * 8 + gc * 2 + x;
-                    float &v = s[n][2 * e + x];
-                    v = u <= tok[e] && u < last ? v : -INFINITY;
-                    top = fmaxf(top, v);
-                }
-            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-            const float base = top == -INFINITY ? 0.0f : top;
-            const float keep = exp2f((mx[e] - base) * p.scale_log2);
-            mx[e] = top;
-            float add = 0.0f;
-#pragma unroll
-            for (int n = 0; n < kKeys / 8; ++n)
-#pragma unroll
-                for (int x = 0; x < 2; ++x) {
-                    float &v = s[n][2 * e + x];
-                    v = exp2f((v - base) * p.scale_log2);
-                    add += v;
-                }
-            sum[e] = sum[e] * keep + add;
-#pragma unroll
-            for (int i = 0; i < D / 8; ++i) {
-                o[i][2 * e] *= keep;
-                o[i][2 * e + 1] *= keep;
-            }
-        }
-#pragma unroll
-        for (int c = 0; c < kKeys / 16; ++c) {
-            const uint32_t a[4] = {pack_bf16x2(s[2 * c][0], s[2 * c][1]), pack_bf16x2(s[2 * c][2], s[2 * c][3]),
-                                   pack_bf16x2(s[2 * c + 1][0], s[2 * c + 1][1]),
-                                   pack_bf16x2(s[2 * c + 1][2], s[2 * c + 1][3])};
-#pragma unroll
-            for (int i = 0; i < D / 8; ++i) {
-                const uint16_t *b = vs + (c * 16 + gc * 2) * kPitch + i * 8 + gr;
-                mma_bf16(o[i], a, (uint32_t)b[0] | ((uint32_t)b[kPitch] << 16),
-                         (uint32_t)b[8 * kPitch] | ((uint32_t)b[9 * kPitch] << 16));
-            }
-        }
-    }
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-        float l = sum[e];
-        l += __shfl_xor_sync(0xffffffffu, l, 1);
-        l += __shfl_xor_sync(0xffffffffu, l, 2);
-        if (!live[e]) continue;
-        const float inv = 1.0f / l;
-        uint16_t *dst = p.o + (row0 + tok[e]) * p.ldo + head[e] * D + gc * 2;
-#pragma unroll
-        for (int i = 0; i < D / 8; ++i)
-            *reinterpret_cast<uint32_t *>(dst + i * 8) = pack_bf16x2(o[i][2 * e] * inv, o[i][2 * e + 1] * inv);
-    }
+    CUtensorMap qm, km, vm;
+    const auto encode = [&](CUtensorMap *map, const uint16_t *base, int64_t heads, int64_t ld, int box_heads, int box_tokens) {
+        return encode_tmap_3d(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, base, D, (uint64_t)heads, (uint64_t)a.M, D * 2,
+                              (uint64_t)ld * 2, 64, (uint32_t)box_heads, (uint32_t)box_tokens, CU_TENSOR_MAP_SWIZZLE_128B);
+    };
+    if (!encode(&qm, q, Hq, ldq, a.r, a.tpt) || !encode(&km, k, a.H, ldk, 1, kKeys) || !encode(&vm, v, a.H, ldv, 1, kKeys))
+        return -1;
+    const int sms = sms_of_device();
+    if (sms == 0) return -2;
+    // at most ceil(len / (2 tpt)) pairs of tiles per sequence
+    const int64_t most = (a.M / (2 * a.tpt) + a.B) * a.H;
+    prompt_attn_kernel<D><<<(unsigned)std::min<int64_t>(most, sms), kThreads, Cfg<D>::kBytes + 1024, st>>>(qm, km, vm, a);
+    return 0;
 }
 
 }  // namespace
@@ -209,15 +519,9 @@ int launch_prompt_attention(const uint16_t *q, int64_t ldq, const uint16_t *k, i
                             int64_t ldv, const int32_t *starts, int64_t B, int64_t M, int64_t Hq, int64_t H, int64_t D,
                             uint16_t *o, int64_t ldo, int *status, cudaStream_t st)
 {
-    (void)status;
-    PromptArgs a{q, k, v, ldq, ldk, ldv, ldo, M, starts, (int)B, (int)H, (int)(Hq / H), 0, 0.0f, o};
-    a.tpt = kRows / a.r;
-    a.scale_log2 = 1.4426950408889634f / sqrtf((float)D);
-    const dim3 grid((unsigned)(M / a.tpt + B), (unsigned)H);
-    const int smem = 2 * kKeys * (int)(D + 8) * 2;
-    if (D == 128) prompt_attn_kernel<128><<<grid, kThreads, smem, st>>>(a);
-    else prompt_attn_kernel<64><<<grid, kThreads, smem, st>>>(a);
-    return 0;
+    const int r = (int)(Hq / H);
+    const PromptArgs a{starts, M, ldo, (int)B, (int)H, r, kRows / r, 1.4426950408889634f / sqrtf((float)D), o, status};
+    return D == 128 ? run<128>(q, ldq, k, ldk, v, ldv, Hq, a, st) : run<64>(q, ldq, k, ldk, v, ldv, Hq, a, st);
 }
 
 }  // namespace wq
