@@ -33,7 +33,7 @@
 // of the tensor core per tile and its 16,384 exponentials as many of the
 // special-function units, so both are at their limits together.
 //
-// Roles (320 threads): warps 0-3 and 4-7 the two softmax warpgroups, warp 8
+// Roles (384 threads, two warps idle): warps 0-3 and 4-7 the two softmax warpgroups, warp 8
 // the copies (Q of the next item as soon as its tile is free, a ring of K and
 // V blocks), warp 9 the MMAs.  Keys past a tile's last visible one are left
 // out of both products in steps of 16; inside the step their p is 0, and V
@@ -51,7 +51,7 @@ namespace {
 
 constexpr int kRows = 128;      // (token, head) rows per tile
 constexpr int kKeys = 128;      // keys per block
-constexpr int kThreads = 320;
+constexpr int kThreads = 384;
 constexpr int kLoadWarp = 8, kMmaWarp = 9;
 constexpr uint32_t kTmemCols = 512;
 constexpr float kSlack = 8.0f;  // log2 of the growth of p that is let pass before m moves
@@ -141,12 +141,22 @@ __device__ __forceinline__ float ex2(float x)
     return y;
 }
 
+__device__ __forceinline__ f32x2 add2_pairs(f32x2 a, f32x2 b)
+{
+    f32x2 r;
+    asm("{\n\t.reg .b64 ra, rb, rd;\n\tmov.b64 ra, {%2, %3};\n\tmov.b64 rb, {%4, %5};\n\t"
+        "add.rn.f32x2 rd, ra, rb;\n\tmov.b64 {%0, %1}, rd;\n\t}"
+        : "=f"(r.x), "=f"(r.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return r;
+}
+
 struct Wait {
     int *status;
     volatile int *abort;
     __device__ __forceinline__ bool operator()(uint64_t *bar, uint32_t parity) const
     {
-        return mbar_wait_fast(bar, parity, status, abort);
+        return mbar_wait(bar, parity, status, abort);
     }
 };
 
@@ -191,8 +201,11 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_consta
     tc_fence_after();
     const uint32_t tmem = b.tmem;  // S of tile x at 128 x, O of tile x at 256 + D x
 
+    // 384 threads of 168 registers at launch: 200 for the softmax warpgroups, 104 for the third
+
     if (wid == kLoadWarp) {
         // ------------------------------ items and copies ------------------------------
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
         Item it{};
         int64_t pairs;
         locate(p, -1, it, pairs);
@@ -258,6 +271,7 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_consta
         (void)ok;
     } else if (wid == kMmaWarp) {
         // ------------------------------ MMAs (lane 0 issues) ------------------------------
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
         uint32_t slot = 0, phase = 0, nitem = 0, qn[2] = {0, 0}, sn[2] = {0, 0}, pvn[2] = {0, 0};
         const uint32_t base = smem_u32(smem);
         bool ok = true;
@@ -363,8 +377,9 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_consta
                 if (global_ns() - t0 > kWaitLimitNs) { record_timeout(p.status); break; }
         }
         __syncwarp();
-    } else {
+    } else if (wid < 8) {
         // ------------------------------ softmax and output, one row per thread ------------------------------
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
         const int x = wid >> 2, row = tid & 127;
         const uint32_t lane_bits = (uint32_t)((wid & 3) * 32) << 16;
         const uint32_t s_addr = tmem + lane_bits + 128u * x, o_addr = tmem + lane_bits + 256u + (uint32_t)D * x;
@@ -386,58 +401,83 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_consta
                 if (!wait(&b.s_full[x], blocks_done & 1u)) { ok = false; break; }
                 tc_fence_after();
                 const int u0 = j * kKeys, keys = min(kKeys, last - u0);
-                uint32_t v[kKeys];
-#pragma unroll
-                for (int c = 0; c < kKeys / 32; ++c)
-                    if (c * 32 < keys) tmem_ld32(s_addr + 32u * c, v + 32 * c);
-                tmem_wait_ld();
-                const bool edge = u0 + kKeys > tile_tok + 1;  // some row does not see every key of the block
-                if (edge) {
-#pragma unroll
-                    for (int c = 0; c < kKeys; ++c)
-                        if (c >= keys || c > tok - u0) v[c] = 0xff800000u;
-                }
-                float top = m;
-#pragma unroll
-                for (int c = 0; c < kKeys; c += 2)
-                    top = fmaxf(top, fmaxf(__uint_as_float(v[c]), __uint_as_float(v[c + 1])));
-                const bool grow = (top - m) * p.scale_log2 > kSlack;
-                if (__any_sync(0xffffffffu, grow)) {
+                // m follows the block's maximum `top` of the row once p would grow by more than 2^kSlack
+                auto move_max = [&](float top) {
+                    const bool grow = (top - m) * p.scale_log2 > kSlack;
+                    if (!__any_sync(0xffffffffu, grow)) return;
                     const float keep = ex2((m - top) * p.scale_log2);
                     m = top;
                     l *= keep;
-                    if (j > 0) {
-                        // the product of the block before has completed: S was issued after it
+                    if (j == 0) return;
+                    // the product of the block before has completed: S was issued after it
 #pragma unroll 1
-                        for (int c = 0; c < D; c += 32) {
-                            uint32_t w[32];
-                            tmem_ld32(o_addr + (uint32_t)c, w);
-                            tmem_wait_ld();
-#pragma unroll
-                            for (int e = 0; e < 32; ++e) w[e] = __float_as_uint(__uint_as_float(w[e]) * keep);
-                            tmem_st32(o_addr + (uint32_t)c, w);
-                        }
-                    }
-                }
-                const float shift = -m * p.scale_log2;
-                const f32x2 sc{p.scale_log2, p.scale_log2}, sh{shift, shift};
-                f32x2 sum[2] = {{0.0f, 0.0f}, {0.0f, 0.0f}};
-#pragma unroll
-                for (int c = 0; c < kKeys / 32; ++c) {
-                    if (c * 32 < keys) {
+                    for (int c = 0; c < D; c += 16) {
                         uint32_t w[16];
+                        tmem_ld16(o_addr + (uint32_t)c, w);
+                        tmem_wait_ld();
 #pragma unroll
-                        for (int e = 0; e < 16; ++e) {
-                            const f32x2 s2{__uint_as_float(v[32 * c + 2 * e]), __uint_as_float(v[32 * c + 2 * e + 1])};
-                            const f32x2 y = fma2_pairs(s2, sc, sh);
-                            const f32x2 q{ex2(y.x), ex2(y.y)};
-                            sum[e & 1] = add2(sum[e & 1], q);
-                            w[e] = pack_bf16x2(q.x, q.y);
-                        }
-                        tmem_st16(s_addr + 16u * c, w);
+                        for (int e = 0; e < 16; ++e) w[e] = __float_as_uint(__uint_as_float(w[e]) * keep);
+                        tmem_st16(o_addr + (uint32_t)c, w);
+                    }
+                };
+                // P and its sum for 32 keys of the row
+                f32x2 sum[2] = {{0.0f, 0.0f}, {0.0f, 0.0f}};
+                auto exponentials = [&](const uint32_t v[32], int c) {
+                    const float shift = -m * p.scale_log2;
+                    const f32x2 sc{p.scale_log2, p.scale_log2}, sh{shift, shift};
+                    uint32_t w[16];
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) {
+                        const f32x2 s2{__uint_as_float(v[2 * e]), __uint_as_float(v[2 * e + 1])};
+                        const f32x2 y = fma2_pairs(s2, sc, sh);
+                        const f32x2 q{ex2(y.x), ex2(y.y)};
+                        sum[e & 1] = add2_pairs(sum[e & 1], q);
+                        w[e] = pack_bf16x2(q.x, q.y);
+                    }
+                    tmem_st16(s_addr + 16u * c, w);
+                };
+                if (u0 + kKeys <= tile_tok + 1) {  // every row sees every key of the block
+                    uint32_t v[kKeys / 32][32];
+#pragma unroll
+                    for (int c = 0; c < kKeys / 32; ++c) tmem_ld32(s_addr + 32u * c, v[c]);
+                    tmem_wait_ld();
+                    float tops[4] = {m, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                    for (int c = 0; c < kKeys / 32; ++c)
+#pragma unroll
+                        for (int e = 0; e < 32; e += 2)
+                            tops[(e / 2) & 3] = fmaxf(tops[(e / 2) & 3], fmaxf(__uint_as_float(v[c][e]), __uint_as_float(v[c][e + 1])));
+                    move_max(fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3])));
+#pragma unroll
+                    for (int c = 0; c < kKeys / 32; ++c) exponentials(v[c], c);
+                } else {
+                    // the last blocks: 32 keys at a time, read once for the maximum and once for P (P of keys
+                    // 32 c .. covers columns of S that were read before)
+                    auto masked = [&](uint32_t v[32], int c) {
+                        tmem_ld32(s_addr + 32u * c, v);
+                        tmem_wait_ld();
+                        const int seen = min(keys, tok - u0 + 1) - 32 * c;
+#pragma unroll
+                        for (int e = 0; e < 32; ++e)
+                            if (e >= seen) v[e] = 0xff800000u;
+                    };
+                    float top = m;
+#pragma unroll 1
+                    for (int c = 0; c * 32 < keys; ++c) {
+                        uint32_t v[32];
+                        masked(v, c);
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) top = fmaxf(top, __uint_as_float(v[e]));
+                    }
+                    move_max(top);
+#pragma unroll 1
+                    for (int c = 0; c * 32 < keys; ++c) {
+                        uint32_t v[32];
+                        masked(v, c);
+                        exponentials(v, c);
                     }
                 }
-                const f32x2 both = add2(sum[0], sum[1]);
+                const f32x2 both = add2_pairs(sum[0], sum[1]);
                 l += both.x + both.y;
                 tmem_wait_st();
                 tc_fence_before();
@@ -470,6 +510,8 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_consta
             }
             tc_fence_before();  // the next item's first product into O follows this warpgroup's next P
         }
+    } else {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
     }
 
     tc_fence_before();
