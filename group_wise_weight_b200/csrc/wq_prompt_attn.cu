@@ -33,12 +33,13 @@
 // of the tensor core per tile and its 16,384 exponentials as many of the
 // special-function units, so both are at their limits together.
 //
-// Roles (384 threads, two warps idle): warps 0-3 and 4-7 the two softmax warpgroups, warp 8
-// the copies (Q of the next item as soon as its tile is free, a ring of K and
-// V blocks), warp 9 the MMAs.  Keys past a tile's last visible one are left
-// out of both products in steps of 16; inside the step their p is 0, and V
-// rows past the sequence's end are zeroed in shared memory, so what lies
-// behind a sequence never enters a sum.  Every barrier wait is bounded.
+// Roles (384 threads, two warps idle): warps 0-3 and 4-7 the two softmax
+// warpgroups, warp 8 the copies (Q of the next item as soon as its tile is
+// free, a ring of K and V blocks), warp 9 the MMAs.
+// Keys past a tile's last visible one are left out of both products in steps
+// of 16; inside the step their p is 0, and the copy warp zeroes the V rows past
+// the sequence's end, so what lies behind a sequence never enters a sum.
+// Every barrier wait is bounded.
 #include <algorithm>
 #include <atomic>
 
@@ -53,6 +54,7 @@ constexpr int kRows = 128;      // (token, head) rows per tile
 constexpr int kKeys = 128;      // keys per block
 constexpr int kThreads = 384;
 constexpr int kLoadWarp = 8, kMmaWarp = 9;
+constexpr int kPart = 64, kParts = kKeys / kPart;  // keys of P that are handed to the tensor core at a time
 constexpr uint32_t kTmemCols = 512;
 constexpr float kSlack = 8.0f;  // log2 of the growth of p that is let pass before m moves
 
@@ -89,7 +91,8 @@ struct Item {
 };
 
 struct Bars {
-    uint64_t kv_full[8], kv_empty[8], q_full[2], q_empty[2], s_full[2], p_full[2], pv_done[2], item_full[2], item_empty[2], done;
+    uint64_t kv_full[8], kv_empty[8], q_full[2], q_empty[2], s_full[2], p_full[2][kParts], pv_done[2], item_full[2],
+        item_empty[2], tail, done;
     Item items[2];
     int abort, pad;
     uint32_t tmem;
@@ -151,6 +154,21 @@ __device__ __forceinline__ f32x2 add2_pairs(f32x2 a, f32x2 b)
     return r;
 }
 
+// One lane of the (whole) warp.
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\tselp.u32 %0, 1, 0, q;\n\t}" : "=r"(p));
+    return p != 0;
+}
+
+__device__ __forceinline__ float max3(float a, float b, float c)
+{
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+
 struct Wait {
     int *status;
     volatile int *abort;
@@ -186,12 +204,13 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_consta
             mbar_init(&b.q_full[i], 1);
             mbar_init(&b.q_empty[i], 1);
             mbar_init(&b.s_full[i], 1);
-            mbar_init(&b.p_full[i], 4);
+            for (int c = 0; c < kParts; ++c) mbar_init(&b.p_full[i][c], 4);
             mbar_init(&b.pv_done[i], 1);
             mbar_init(&b.item_full[i], 1);
             mbar_init(&b.item_empty[i], 9);  // 8 softmax warps and the MMA warp
         }
         mbar_init(&b.done, 1);
+        mbar_init(&b.tail, 1);
         b.abort = 0;
         fence_mbar_init();
     }
@@ -210,7 +229,7 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_consta
         int64_t pairs;
         locate(p, -1, it, pairs);
         const int64_t total = pairs * p.H;
-        uint32_t slot = 0, phase = 0, loads = 0, nitem = 0, qn[2] = {0, 0};
+        uint32_t slot = 0, phase = 0, loads = 0, nitem = 0, tails = 0, qn[2] = {0, 0};
         bool ok = true;
         for (int64_t i = blockIdx.x;; i += gridDim.x) {
             const uint32_t s = nitem & 1u;
@@ -243,11 +262,26 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_consta
             };
             auto load_kv = [&](const CUtensorMap *map, int j) {
                 if (loads >= S && !wait(&b.kv_empty[slot], phase ^ 1u)) return false;
+                uint8_t *dst = smem + C::kRing + slot * C::kTileBytes;
+                // V rows past the sequence's end within a step of 16 keys (the products leave later ones out)
+                const int in_seq = it.len - j * kKeys;
+                const bool tail = map == &vmap && in_seq < kKeys && (in_seq & 15);
+                uint64_t *bar = tail ? &b.tail : &b.kv_full[slot];
                 if (lane == 0) {
-                    mbar_arrive_expect_tx(&b.kv_full[slot], (uint32_t)C::kTileBytes);
+                    mbar_arrive_expect_tx(bar, (uint32_t)C::kTileBytes);
                     for (int c = 0; c < C::kCols; ++c)
-                        tma_load_3d(smem + C::kRing + slot * C::kTileBytes + c * C::kBlkBytes, map, &b.kv_full[slot],
-                                    c * 64, it.h, (int)it.row0 + j * kKeys);
+                        tma_load_3d(dst + c * C::kBlkBytes, map, bar, c * 64, it.h, (int)it.row0 + j * kKeys);
+                }
+                if (tail) {
+                    const bool landed = wait(&b.tail, tails++ & 1u);
+                    const int chunks = (16 - (in_seq & 15)) * 8;  // of 16 bytes, per column block
+                    for (int i = lane; i < chunks * C::kCols; i += 32)
+                        *reinterpret_cast<uint4 *>(dst + i / chunks * C::kBlkBytes + in_seq * 128 + i % chunks * 16) =
+                            make_uint4(0u, 0u, 0u, 0u);
+                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&b.kv_full[slot]);
+                    if (!landed) return false;
                 }
                 ++loads;
                 if (++slot == S) { slot = 0; phase ^= 1u; }
@@ -267,110 +301,108 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_consta
             for (uint32_t j = loads > S ? loads - S : 0; j < loads; ++j) drain(&b.kv_full[j % S], (j / S) & 1u);
             for (int x = 0; x < 2; ++x)
                 if (qn[x] > 0) drain(&b.q_full[x], (qn[x] - 1) & 1u);
+            if (tails > 0) drain(&b.tail, (tails - 1) & 1u);
         }
-        (void)ok;
     } else if (wid == kMmaWarp) {
-        // ------------------------------ MMAs (lane 0 issues) ------------------------------
+        // ------------------------------ MMAs: one thread ------------------------------
         asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
-        uint32_t slot = 0, phase = 0, nitem = 0, qn[2] = {0, 0}, sn[2] = {0, 0}, pvn[2] = {0, 0};
-        const uint32_t base = smem_u32(smem);
-        bool ok = true;
-        auto next_slot = [&]() {
-            if (++slot == S) { slot = 0; phase ^= 1u; }
-        };
-        while (ok) {
-            const uint32_t is = nitem & 1u;
-            if (!wait(&b.item_full[is], (nitem >> 1) & 1u)) break;
-            const Item it = b.items[is];
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&b.item_empty[is]);
-            ++nitem;
-            if (!it.valid) break;
-            const int nb[2] = {it.blocks(0, p.tpt), it.blocks(1, p.tpt)}, n = std::max(nb[0], nb[1]);
-            // S of tile x and block j (its K in ring slot `ks`): S's columns hold the P of the block before, which its
+        if (elect_one()) {
+            uint32_t slot = 0, phase = 0, nitem = 0;
+            uint32_t qn0 = 0, qn1 = 0, pn0 = 0, pn1 = 0;  // per tile: Q tiles and blocks so far
+            uint32_t parts0 = 0, parts1 = 0;              // bit c: the next parity of part c of P
+            const uint32_t base = smem_u32(smem);
+            bool ok = true;
+            auto next_slot = [&]() {
+                if (++slot == S) { slot = 0; phase ^= 1u; }
+            };
+            // S of tile x for `keys` keys of the K block at k: S's columns hold the P of the block before, which its
             // product must have read
-            auto qk = [&](int x, int j, uint32_t ks) {
-                if (pvn[x] > 0 && !wait(&b.pv_done[x], (pvn[x] - 1) & 1u)) return false;
+            auto scores = [&](int x, uint32_t k, int keys, uint32_t pn) {
+                if (pn > 0 && !wait(&b.pv_done[x], (pn - 1) & 1u)) return false;
                 tc_fence_after();
-                if (lane == 0) {
-                    const int keys = min(kKeys, it.last(x, p.tpt) - j * kKeys);
-                    const uint32_t idesc = idesc_qk((keys + 15) & ~15);
-                    const uint32_t q = base + x * C::kTileBytes, k = base + C::kRing + ks * C::kTileBytes;
+                const uint32_t idesc = idesc_qk((keys + 15) & ~15);
+                const uint32_t q = base + x * C::kTileBytes;
 #pragma unroll
-                    for (int e = 0; e < D / 16; ++e) {
-                        const uint32_t off = (uint32_t)(e / 4 * C::kBlkBytes + e % 4 * 32);
-                        tc_mma_ss(tmem + 128u * x, smem_desc(q + off, 16, 1024, 2), smem_desc(k + off, 16, 1024, 2), idesc, e > 0);
+                for (int e = 0; e < D / 16; ++e) {
+                    const uint32_t off = (uint32_t)(e / 4 * C::kBlkBytes + e % 4 * 32);
+                    tc_mma_ss(tmem + 128u * x, smem_desc(q + off, 16, 1024, 2), smem_desc(k + off, 16, 1024, 2), idesc, e > 0);
+                }
+                tc_commit(&b.s_full[x]);
+                return true;
+            };
+            // O += P V, part by part as P comes
+            auto product = [&](int x, uint32_t v, int keys, bool first, uint32_t &parts) {
+#pragma unroll
+                for (int c = 0; c < kParts; ++c) {
+                    if (c * kPart < keys) {
+                        if (!wait(&b.p_full[x][c], (parts >> c) & 1u)) return false;
+                        parts ^= 1u << c;
+                        tc_fence_after();
+#pragma unroll
+                        for (int e = c * (kPart / 16); e < (c + 1) * (kPart / 16); ++e)
+                            if (e * 16 < keys)
+                                tc_mma_ts(tmem + 256u + (uint32_t)D * x, tmem + 128u * x + 8u * e,
+                                          smem_desc(v + 2048u * e, C::kBlkBytes, 1024, 2), idesc_pv(D), (!first || e > 0) ? 1u : 0u);
                     }
-                    tc_commit(&b.s_full[x]);
-                    if (j + 1 == nb[x]) tc_commit(&b.q_empty[x]);
                 }
-                __syncwarp();
-                ++sn[x];
+                tc_commit(&b.pv_done[x]);
                 return true;
             };
-            auto pv = [&](int x, int j, uint32_t vs) {
-                if (!wait(&b.p_full[x], pvn[x] & 1u)) return false;
-                tc_fence_after();
-                if (lane == 0) {
-                    const int keys = min(kKeys, it.last(x, p.tpt) - j * kKeys);
-                    const uint32_t v = base + C::kRing + vs * C::kTileBytes;
-#pragma unroll
-                    for (int e = 0; e < kKeys / 16; ++e)
-                        if (e * 16 < keys)
-                            tc_mma_ts(tmem + 256u + (uint32_t)D * x, tmem + 128u * x + 8u * e,
-                                      smem_desc(v + 2048u * e, C::kBlkBytes, 1024, 2), idesc_pv(D), (j > 0 || e > 0) ? 1u : 0u);
-                    tc_commit(&b.pv_done[x]);
-                }
-                __syncwarp();
-                ++pvn[x];
-                return true;
-            };
-            auto release = [&](uint32_t s) {
-                if (lane == 0) tc_commit(&b.kv_empty[s]);
-                __syncwarp();
-            };
-            // Q and the first K
-            uint32_t ks = slot;
-            ok = wait(&b.q_full[0], qn[0]++ & 1u) && wait(&b.kv_full[slot], phase) && qk(0, 0, ks);
-            next_slot();
-            if (ok && nb[1] > 0) ok = wait(&b.q_full[1], qn[1]++ & 1u) && qk(1, 0, ks);
-            if (!ok) break;
-            release(ks);
-            for (int j = 0; ok && j < n; ++j) {
-                const uint32_t vs = slot;
-                ok = wait(&b.kv_full[vs], phase);
+            while (ok) {
+                const uint32_t is = nitem & 1u;
+                if (!wait(&b.item_full[is], (nitem >> 1) & 1u)) break;
+                const Item it = b.items[is];
+                mbar_arrive(&b.item_empty[is]);
+                ++nitem;
+                if (!it.valid) break;
+                const int last0 = it.last(0, p.tpt), last1 = it.last(1, p.tpt);
+                const int nb0 = it.blocks(0, p.tpt), nb1 = it.blocks(1, p.tpt), n = std::max(nb0, nb1);
+                // Q and the first K
+                uint32_t k = base + C::kRing + slot * C::kTileBytes;
+                ok = wait(&b.q_full[0], qn0++ & 1u) && wait(&b.kv_full[slot], phase) && scores(0, k, min(kKeys, last0), pn0);
                 if (!ok) break;
+                if (nb0 == 1) tc_commit(&b.q_empty[0]);
+                if (nb1 > 0) {
+                    ok = wait(&b.q_full[1], qn1++ & 1u) && scores(1, k, min(kKeys, last1), pn1);
+                    if (nb1 == 1) tc_commit(&b.q_empty[1]);
+                }
+                if (!ok) break;
+                tc_commit(&b.kv_empty[slot]);
                 next_slot();
-                const int in_seq = it.len - j * kKeys;  // V rows from here on are no part of the sequence
-                if (in_seq < kKeys && (in_seq & 15)) {
-                    const int rows = 16 - (in_seq & 15);
-                    for (int i = lane; i < rows * 8 * C::kCols; i += 32) {
-                        const int c = i / (rows * 8), w = i % (rows * 8);
-                        *reinterpret_cast<uint4 *>(smem + C::kRing + vs * C::kTileBytes + c * C::kBlkBytes + in_seq * 128 + w * 16) =
-                            make_uint4(0u, 0u, 0u, 0u);
-                    }
-                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                    __syncwarp();
-                }
-                const uint32_t k1 = slot;
-                bool have_k = false;
-                for (int x = 0; ok && x < 2; ++x) {
-                    if (j < nb[x]) ok = pv(x, j, vs);
-                    if (ok && j + 1 < nb[x]) {
-                        if (!have_k) ok = wait(&b.kv_full[k1], phase);
-                        have_k = true;
-                        ok = ok && qk(x, j + 1, k1);
-                    }
-                }
-                if (!ok) break;
-                release(vs);
-                if (j + 1 < n) {
+                // Tile 0's product and next S, then tile 1's: the strict order keeps the tiles half a period apart
+                for (int j = 0; j < n; ++j) {
+                    const uint32_t vs = slot, v = base + C::kRing + vs * C::kTileBytes;
+                    const int u0 = j * kKeys, u1 = u0 + kKeys;
+                    ok = wait(&b.kv_full[vs], phase);
+                    if (!ok) break;
                     next_slot();
-                    release(k1);
+                    if (j < nb0) {
+                        ok = product(0, v, min(kKeys, last0 - u0), j == 0, parts0);
+                        ++pn0;
+                    }
+                    if (ok && j + 1 < n) ok = wait(&b.kv_full[slot], phase);
+                    k = base + C::kRing + slot * C::kTileBytes;
+                    if (ok && j + 1 < nb0) {
+                        ok = scores(0, k, min(kKeys, last0 - u1), pn0);
+                        if (j + 2 == nb0) tc_commit(&b.q_empty[0]);
+                    }
+                    if (ok && j < nb1) {
+                        ok = product(1, v, min(kKeys, last1 - u0), j == 0, parts1);
+                        ++pn1;
+                    }
+                    if (!ok) break;
+                    tc_commit(&b.kv_empty[vs]);
+                    if (j + 1 < nb1) {
+                        ok = scores(1, k, min(kKeys, last1 - u1), pn1);
+                        if (j + 2 == nb1) tc_commit(&b.q_empty[1]);
+                    }
+                    if (!ok) break;
+                    if (j + 1 < n) {
+                        tc_commit(&b.kv_empty[slot]);
+                        next_slot();
+                    }
                 }
             }
-        }
-        if (lane == 0) {
             tc_commit(&b.done);
             const uint64_t t0 = global_ns();
             while (!mbar_try_wait(&b.done, 0))  // every MMA must complete before tensor memory is released
@@ -436,6 +468,12 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_consta
                     }
                     tmem_st16(s_addr + 16u * c, w);
                 };
+                auto hand_over = [&](int part) {
+                    tmem_wait_st();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&b.p_full[x][part]);
+                };
                 if (u0 + kKeys <= tile_tok + 1) {  // every row sees every key of the block
                     uint32_t v[kKeys / 32][32];
 #pragma unroll
@@ -446,10 +484,13 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_consta
                     for (int c = 0; c < kKeys / 32; ++c)
 #pragma unroll
                         for (int e = 0; e < 32; e += 2)
-                            tops[(e / 2) & 3] = fmaxf(tops[(e / 2) & 3], fmaxf(__uint_as_float(v[c][e]), __uint_as_float(v[c][e + 1])));
+                            tops[(e / 2) & 3] = max3(tops[(e / 2) & 3], __uint_as_float(v[c][e]), __uint_as_float(v[c][e + 1]));
                     move_max(fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3])));
 #pragma unroll
-                    for (int c = 0; c < kKeys / 32; ++c) exponentials(v[c], c);
+                    for (int c = 0; c < kKeys / 32; ++c) {
+                        exponentials(v[c], c);
+                        if ((c + 1) * 32 % kPart == 0) hand_over((c + 1) * 32 / kPart - 1);
+                    }
                 } else {
                     // the last blocks: 32 keys at a time, read once for the maximum and once for P (P of keys
                     // 32 c .. covers columns of S that were read before)
@@ -467,7 +508,7 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_consta
                         uint32_t v[32];
                         masked(v, c);
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) top = fmaxf(top, __uint_as_float(v[e]));
+                        for (int e = 0; e < 32; e += 2) top = max3(top, __uint_as_float(v[e]), __uint_as_float(v[e + 1]));
                     }
                     move_max(top);
 #pragma unroll 1
@@ -475,14 +516,11 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_consta
                         uint32_t v[32];
                         masked(v, c);
                         exponentials(v, c);
+                        if ((c + 1) * 32 % kPart == 0 || (c + 1) * 32 >= keys) hand_over(c * 32 / kPart);
                     }
                 }
                 const f32x2 both = add2_pairs(sum[0], sum[1]);
                 l += both.x + both.y;
-                tmem_wait_st();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&b.p_full[x]);
                 ++blocks_done;
             }
             if (!ok) break;
