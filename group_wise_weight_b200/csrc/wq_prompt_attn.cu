@@ -63,9 +63,10 @@ struct Cfg {
     static constexpr int kCols = D / 64;               // 128-byte column blocks of a row
     static constexpr int kBlkBytes = kRows * 128;      // one column block of 128 rows
     static constexpr int kTileBytes = kCols * kBlkBytes;
-    static constexpr int kStages = D == 128 ? 5 : 8;   // K and V blocks in the ring
+    static constexpr int kStages = D == 128 ? 4 : 8;   // K and V blocks in the ring
     static constexpr int kRing = 2 * kTileBytes;       // after the two Q tiles
-    static constexpr int kBarOff = kRing + kStages * kTileBytes;
+    static constexpr int kOutOff = kRing + kStages * kTileBytes;  // 32 rows of 32 output values per softmax warp
+    static constexpr int kBarOff = kOutOff + 8 * 32 * 64;
     static constexpr int kBytes = kBarOff + 512;
 };
 
@@ -529,22 +530,37 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_consta
             tc_fence_after();
             const float inv = 1.0f / l;
             const bool live = row < p.tpt * p.r && tok < it.len;
-            uint16_t *dst = p.o + (it.row0 + tok) * p.ldo + (it.h * p.r + row_head) * D;
+            // 32 output values of a row at a time, through shared memory (16-byte pieces at piece ^ (row / 2) % 4 of
+            // the row's 64 bytes: no bank conflicts either way), so that a store instruction writes 8 rows' 64
+            // adjacent bytes and not 32 rows' 16
+            uint8_t *out = smem + C::kOutOff + wid * (32 * 64);
+            const uint64_t dst = reinterpret_cast<uint64_t>(p.o + (it.row0 + tok) * p.ldo + (it.h * p.r + row_head) * D);
+            const uint32_t alive = __ballot_sync(0xffffffffu, live);
+            const int piece = lane & 3;
+            uint64_t to[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) to[i] = __shfl_sync(0xffffffffu, dst, 8 * i + (lane >> 2)) + 16u * piece;
 #pragma unroll 1
             for (int c = 0; c < D; c += 32) {
                 uint32_t w[32];
                 tmem_ld32(o_addr + (uint32_t)c, w);
                 tmem_wait_ld();
-                if (live) {
 #pragma unroll
-                    for (int e = 0; e < 32; e += 8) {
-                        uint32_t h[4];
+                for (int e = 0; e < 4; ++e) {
+                    uint32_t g[4];
 #pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            h[i] = pack_bf16x2(__uint_as_float(w[e + 2 * i]) * inv, __uint_as_float(w[e + 2 * i + 1]) * inv);
-                        *reinterpret_cast<uint4 *>(dst + c + e) = make_uint4(h[0], h[1], h[2], h[3]);
-                    }
+                    for (int i = 0; i < 4; ++i)
+                        g[i] = pack_bf16x2(__uint_as_float(w[8 * e + 2 * i]) * inv, __uint_as_float(w[8 * e + 2 * i + 1]) * inv);
+                    *reinterpret_cast<uint4 *>(out + lane * 64 + (e ^ ((lane >> 1) & 3)) * 16) = make_uint4(g[0], g[1], g[2], g[3]);
                 }
+                __syncwarp();
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int r = 8 * i + (lane >> 2);
+                    const uint4 g = *reinterpret_cast<const uint4 *>(out + r * 64 + (piece ^ ((r >> 1) & 3)) * 16);
+                    if ((alive >> r) & 1u) *reinterpret_cast<uint4 *>(to[i] + 2u * c) = g;
+                }
+                __syncwarp();
             }
             tc_fence_before();  // the next item's first product into O follows this warpgroup's next P
         }
