@@ -570,6 +570,7 @@ int launch_gemm_w8a8_int8(const int8_t *xq, const float *xscales, int64_t M, int
     a.M = M; a.N = N; a.K = K;
     a.xs = xscales; a.ws16 = wscales;
     a.y = y; a.status = status;
+    if (gemm_i8_pair_eligible(M, N, K)) return launch_gemm_i8_pair(xq, xscales, M, N, K, wq, wscales, y, status, st);
     const uint8_t *x = reinterpret_cast<const uint8_t *>(xq), *w = reinterpret_cast<const uint8_t *>(wq);
     switch (fp8_bn(M)) {
     case 32: return run<32, kInt8>(x, w, a, workspace, st);

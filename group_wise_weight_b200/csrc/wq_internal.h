@@ -173,6 +173,11 @@ size_t gemm_int8_workspace_bytes(int64_t M, int64_t N, int64_t K);
 int launch_gemm_w8a8_int8(const int8_t *xq, const float *xscales, int64_t M, int64_t N, int64_t K, const int8_t *wq,
                           const uint16_t *wscales, uint16_t *y, void *workspace, int *status, cudaStream_t st);
 
+// The same on pairs of SMs (wq_gemm_i8.cu), for many rows: no workspace.
+bool gemm_i8_pair_eligible(int64_t M, int64_t N, int64_t K);
+int launch_gemm_i8_pair(const int8_t *xq, const float *xscales, int64_t M, int64_t N, int64_t K, const int8_t *wq,
+                        const uint16_t *wscales, uint16_t *y, int *status, cudaStream_t st);
+
 // Per-head norms and rotary positions of queries and keys (wq_rope.cu): D in {64, 128}, rot a multiple of 16.
 // qw, kw: both null for positions alone.
 void launch_qk_norm_rope(const uint16_t *q, int64_t ldq, const uint16_t *k, int64_t ldk, const uint16_t *qw,
