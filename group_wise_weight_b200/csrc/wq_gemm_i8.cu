@@ -1,27 +1,40 @@
-// wq_gemm_i8.cu -- INT8 W8A8 matmul for many rows of activations, on pairs
-// of SMs (sm_100a, tcgen05.mma kind::i8 with cta_group::2).
+// wq_gemm_i8.cu -- INT8 W8A8 matmul on the 5th-generation tensor cores
+// (sm_100a, tcgen05.mma kind::i8).
 //
 //   y[m][n] = bf16( float(sum_k xq[m][k] wq[n][k]) * (sx[m] * sw[n]) ),
 // sums exact 32-bit integers ("Quantization Methods Compared: INT8, GPTQ,
 // AWQ, FP8, FP4 and KV-Cache Quantization", section "What quantisation does":
 // the product of the codes, scaled; here a scale per token and per channel).
 //
-// With many rows the tensor cores bound the product, provided the operands
-// reach them: at 8,192 int8 multiply-adds per cycle an SM that computes a
-// 128 x 256 tile alone takes in 96 bytes per cycle, more than L2 gives every SM
-// at once.  A pair of CTAs computes 256 x 256: each holds the accumulators of
-// its 128 rows of activations and loads those and half of the tile's 256
-// weight rows; the pair's MMA reads both halves, so an SM takes in 64 bytes
-// per cycle.
+// Two kernels, both persistent, both fed by TMA with the 128-byte swizzle in
+// stages of 128 bytes of K (past K's end a copy fills in zeros, which add
+// nothing), accumulators double-buffered in tensor memory, every barrier wait
+// bounded (but the pair's two cluster barriers, which every thread reaches).
 //
-// Per CTA (192 threads): warp 0 copies stages of 128 bytes of K by TMA (128-byte
-// swizzle) into a ring, its completions counted by the leader CTA's barrier;
-// in the leader, one thread of warp 1 issues the pair's MMAs and their commits,
-// which reach both CTAs; warps 2-5 turn one of two accumulators in tensor
-// memory into bf16 while the MMAs fill the other.  Tiles are taken round-robin
-// in an order that walks the weight columns within a band of activation rows
-// small enough to stay in L2.  Every barrier wait is bounded (but the two
-// cluster barriers, which every thread reaches).
+// Few rows (gemm_i8_stream_kernel): the weights are read once and bound the
+// call, so the work is cut along K as well: units of (tile, stage) in tile
+// order, dealt evenly over the SMs.  A tile is 128 or 256 weight rows (the
+// MMA's M, so a token costs one of its N columns) by 16 to 128 tokens; 256
+// weight rows where the tokens' own bytes would weigh on L2.  A CTA
+// that holds part of a tile leaves its integer sums in the workspace and adds
+// its stages to the tile's counter; the one that completes the counter adds
+// the parts up (exact, so in any order) and writes y.  Nobody waits for
+// anybody.  The kernel is launched to overlap the previous one's end: before
+// that has completed it only asks L2 to fetch its first weights (a hint; no
+// value read).
+//
+// Many rows (gemm_i8_pair_kernel): the tensor cores bound the product, provided
+// the operands reach them: at 8,192 int8 multiply-adds per cycle an SM that
+// computes a 128 x 256 tile alone takes in 96 bytes per cycle, more than L2
+// gives every SM at once.  A pair of CTAs computes 256 x 256: each holds the
+// accumulators of its 128 rows of activations and loads those and half of the
+// tile's 256 weight rows; the pair's MMA reads both halves, so an SM takes in
+// 64 bytes per cycle.  Warp 0 of each CTA copies, its completions counted by
+// the leader CTA's barrier; in the leader, one thread of warp 1 issues the
+// pair's MMAs and their commits, which reach both CTAs; warps 2-5 turn one of
+// two accumulators into bf16 while the MMAs fill the other.  Tiles are taken
+// round-robin in an order that walks the weight columns within a band of
+// activation rows small enough to stay in L2.
 #include <algorithm>
 #include <atomic>
 
@@ -232,7 +245,7 @@ gemm_i8_pair_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_const
         __syncwarp();
     } else {
         // ------------------------------ epilogue: one row per thread ------------------------------
-        const int quarter = wid & 3, row = quarter * 32 + lane, et = tid - 64;
+        const int quarter = wid & 3, et = tid - 64;
         const uint32_t lane_bits = (uint32_t)(quarter * 32) << 16;
         uint8_t *out = smem + kOutOff + (wid - 2) * kOutBytes;
         float *sw = reinterpret_cast<float *>(smem + kScaleOff);
@@ -301,7 +314,319 @@ gemm_i8_pair_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_const
     if (wid == 1) asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u) : "memory");
 }
 
-// SMs of the current device; the kernel's shared-memory limit is raised on its first use there.
+// ------------------------------------------------------------------------------------------------------------
+// Few rows
+// ------------------------------------------------------------------------------------------------------------
+
+// D (+)= A B^T on one CTA, signed bytes, 32 of K.
+__device__ __forceinline__ void mma_one(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc, uint32_t accumulate)
+{
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+                 "tcgen05.mma.cta_group::1.kind::i8 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+                 "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+                 : "memory");
+}
+
+__device__ __forceinline__ void prefetch_l2(const CUtensorMap *map, int x, int y)
+{
+    asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global [%0, {%1, %2}];" ::"l"(map), "r"(x), "r"(y) : "memory");
+}
+
+// BN tokens by 128 weight rows.  The narrow tiles leave room for the next call's CTA beside this one.
+template <int BN>
+struct Stream {
+    static constexpr int kStage = kOperand + BN * kRowBytes;
+    static constexpr int kStages = BN == 16 ? 6 : BN == 32 ? 5 : BN == 64 ? 8 : 6;
+    static constexpr int kBarOff = kStages * kStage;
+    static constexpr int kSmem = kBarOff + 256;
+    static constexpr bool kSliced = BN >= 64;  // who adds up a split tile: its CTAs, a share each, or the last to finish
+    static constexpr uint32_t kCols = 2 * BN;  // two accumulators
+};
+
+constexpr int kReader = 1 << 20;  // a counter's unit for CTAs that have read their share (the stages stay below it)
+constexpr int kColumns = 4;       // columns in flight per warp of the sliced sum
+
+// Device-scope load with acquire semantics: later reads see what was written before the matching add.
+__device__ __forceinline__ int ld_acquire(const int *p)
+{
+    int v;
+    asm volatile("ld.acquire.gpu.global.s32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+    return v;
+}
+
+struct StreamBars {
+    uint64_t full[8], empty[8], d_full[2], d_empty[2], done;
+    int abort, last;
+    uint32_t tmem;
+};
+static_assert(sizeof(StreamBars) <= 256, "the barrier area");
+
+// Units (tile, stage) in tile order; CTA b takes `per` of them, the first `extra` CTAs one more, the last what is left.
+struct Plan {
+    int64_t tiles, total;
+    int nt, stages, grid, per, extra, max_segs;
+    __host__ __device__ int64_t begin_of(int b) const
+    {
+        const int64_t u = (int64_t)b * per + (b < extra ? b : extra);
+        return u < total ? u : total;
+    }
+    __host__ __device__ int cta_of(int64_t u) const
+    {
+        const int64_t big = (int64_t)extra * (per + 1);
+        return (int)(u < big ? u / (per + 1) : extra + (u - big) / per);
+    }
+};
+
+struct StreamArgs {
+    Args g;
+    Plan plan;
+    int *counters, *part;
+};
+
+template <int BN>
+__global__ void __launch_bounds__(kThreads)
+gemm_i8_stream_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CUtensorMap wmap, const StreamArgs p)
+{
+    using C = Stream<BN>;
+    constexpr uint32_t S = (uint32_t)C::kStages;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
+    StreamBars &b = *reinterpret_cast<StreamBars *>(smem + C::kBarOff);
+    const int tid = threadIdx.x, wid = tid >> 5, lane = tid & 31, stages = p.plan.stages, nt = p.plan.nt;
+    const int64_t beg = p.plan.begin_of(blockIdx.x), end = p.plan.begin_of(blockIdx.x + 1);
+    auto wait = [&](uint64_t *bar, uint32_t parity) { return mbar_wait(bar, parity, p.g.status, &b.abort); };
+
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    if (tid == 0) {
+        for (uint32_t i = 0; i < S; ++i) {
+            mbar_init(&b.full[i], 1);
+            mbar_init(&b.empty[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&b.d_full[i], 1);
+            mbar_init(&b.d_empty[i], 4);
+        }
+        mbar_init(&b.done, 1);
+        b.abort = 0;
+        fence_mbar_init();
+    }
+    if (wid == 0 && lane < (int)S && beg + lane < end) {
+        const int64_t tile = (beg + lane) / stages;
+        const int s = (int)(beg + lane - tile * stages);
+        prefetch_l2(&wmap, s * kRowBytes, (int)(tile % nt) * 128);
+    }
+    if (wid == 1) tmem_alloc(&b.tmem, C::kCols);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = b.tmem;
+    asm volatile("griddepcontrol.wait;" ::: "memory");  // what came before on the stream is complete from here on
+
+    if (wid == 0) {
+        // ------------------------------ copies ------------------------------
+        if (elect_one()) {
+            uint32_t slot = 0, phase = 0, issued = 0;
+            int64_t tile = beg / stages;
+            int s = (int)(beg - tile * stages);
+            for (int64_t u = beg; u < end; ++u) {
+                if (issued >= S && !wait(&b.empty[slot], phase ^ 1u)) break;
+                uint8_t *st = smem + slot * C::kStage;
+                const int n = (int)(tile % nt) * 128, m = (int)(tile / nt) * BN;
+                mbar_arrive_expect_tx(&b.full[slot], C::kStage);
+                tma_load_2d(st, &wmap, &b.full[slot], s * kRowBytes, n);
+                tma_load_2d(st + kOperand, &xmap, &b.full[slot], s * kRowBytes, m);
+                ++issued;
+                if (++slot == S) { slot = 0; phase ^= 1u; }
+                if (++s == stages) { s = 0; ++tile; }
+            }
+            // every issued copy must land before the CTA may exit (bounded, ignoring abort)
+            for (uint32_t j = issued > S ? issued - S : 0; j < issued; ++j) {
+                const uint64_t t0 = global_ns();
+                while (!mbar_try_wait(&b.full[j % S], (j / S) & 1u))
+                    if (global_ns() - t0 > kWaitLimitNs) { record_timeout(p.g.status); break; }
+            }
+        }
+        __syncwarp();
+    } else if (wid == 1) {
+        // ------------------------------ MMAs: one thread ------------------------------
+        if (elect_one()) {
+            uint32_t slot = 0, phase = 0, n = 0;
+            const uint32_t base = smem_u32(smem);
+            constexpr uint32_t idesc = idesc_s8_s32(128, BN);
+            bool ok = true;
+            for (int64_t u = beg; ok && u < end; ++n) {
+                const int s0 = (int)(u % stages), s1 = (int)std::min<int64_t>(stages, s0 + (end - u));
+                const uint32_t d = tmem + (n & 1u) * (uint32_t)BN;
+                if (n >= 2 && !wait(&b.d_empty[n & 1u], ((n >> 1) - 1) & 1u)) break;
+                tc_fence_after();
+                for (int s = s0; s < s1; ++s) {
+                    if (!wait(&b.full[slot], phase)) { ok = false; break; }
+                    tc_fence_after();
+                    const uint32_t w = base + slot * C::kStage, x = w + kOperand;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        mma_one(d, smem_desc(w + 32u * e, 16, 1024, 2), smem_desc(x + 32u * e, 16, 1024, 2), idesc,
+                                (s > s0 || e > 0) ? 1u : 0u);
+                    tc_commit(&b.empty[slot]);
+                    if (++slot == S) { slot = 0; phase ^= 1u; }
+                }
+                if (ok) tc_commit(&b.d_full[n & 1u]);
+                u += s1 - s0;
+            }
+            tc_commit(&b.done);
+            const uint64_t t0 = global_ns();
+            while (!mbar_try_wait(&b.done, 0))  // every MMA must complete before tensor memory is released
+                if (global_ns() - t0 > kWaitLimitNs) { record_timeout(p.g.status); break; }
+        }
+        __syncwarp();
+    } else {
+        // ------------------------------ epilogue: one weight row per thread ------------------------------
+        const int quarter = wid & 3, r = quarter * 32 + lane;
+        const uint32_t lane_bits = (uint32_t)(quarter * 32) << 16;
+        const int64_t M = p.g.M, N = p.g.N;
+        uint32_t n = 0;
+        bool ok = true;
+        for (int64_t u = beg; u < end; ++n) {
+            const int64_t tile = u / stages;
+            const int s0 = (int)(u - tile * stages), s1 = (int)std::min<int64_t>(stages, s0 + (end - u));
+            const int64_t nr = tile % nt * 128 + r, m0 = tile / nt * BN;
+            const int cols = (int)std::min<int64_t>(BN, M - m0);
+            if (!wait(&b.d_full[n & 1u], (n >> 1) & 1u)) { ok = false; break; }
+            tc_fence_after();
+            const uint32_t d = tmem + lane_bits + (n & 1u) * (uint32_t)BN;
+            const bool whole = s0 == 0 && s1 == stages;
+            // the tile's parts: [part][column][row]
+            int *parts = p.part + tile * p.plan.max_segs * (BN * 128);
+            const int first = p.plan.cta_of(tile * stages), mine = (int)blockIdx.x - first;
+            const int count = whole ? 1 : p.plan.cta_of(tile * stages + stages - 1) - first + 1;
+            bool writes = whole;  // sliced tiles are written below
+            if (!whole) {
+#pragma unroll 1
+                for (int c = 0; c < cols; c += 16) {
+                    uint32_t v[16];
+                    tmem_ld16(d + (uint32_t)c, v);
+                    tmem_wait_ld();
+                    int *to = parts + ((int64_t)mine * BN + c) * 128 + r;
+#pragma unroll
+                    for (int e = 0; e < 16; ++e)
+                        if (c + e < cols) to[e * 128] = (int)v[e];
+                }
+                __threadfence();
+                named_bar_sync(1, 128);
+                if (C::kSliced) {
+                    if (tid == 64) atomicAdd(p.counters + tile, s1 - s0);
+                } else {
+                    if (tid == 64) b.last = atomicAdd(p.counters + tile, s1 - s0) + (s1 - s0) == stages;
+                    named_bar_sync(1, 128);
+                    writes = *(volatile int *)&b.last != 0;
+                    if (writes) __threadfence();
+                }
+            }
+            if (writes) {
+                const float sw = nr < N ? bf16_to_f32(ld_nc_u16(p.g.ws + nr)) : 0.0f;
+#pragma unroll 1
+                for (int c = 0; c < cols; c += 16) {
+                    uint32_t v[16];
+                    tmem_ld16(d + (uint32_t)c, v);
+                    tmem_wait_ld();
+                    for (int o = 0; o < count; ++o) {
+                        if (o == mine) continue;
+                        const int *from = parts + ((int64_t)o * BN + c) * 128 + r;
+#pragma unroll
+                        for (int e = 0; e < 16; ++e)
+                            if (c + e < cols) v[e] += (uint32_t)__ldcg(from + e * 128);
+                    }
+                    if (nr < N) {
+#pragma unroll
+                        for (int e = 0; e < 16; ++e)
+                            if (c + e < cols)
+                                p.g.y[(m0 + c + e) * N + nr] =
+                                    f32_to_bf16(__fmul_rn((float)(int)v[e], __fmul_rn(__ldg(p.g.xs + m0 + c + e), sw)));
+                    }
+                }
+                if (!whole && tid == 64) p.counters[tile] = 0;  // every part has been counted: nobody else touches it
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&b.d_empty[n & 1u]);
+            u += s1 - s0;
+        }
+        if (C::kSliced && ok) {
+            // the split tiles, first and last of this CTA's range: its share of their columns
+            for (int e = 0; e < 2; ++e) {
+                const int64_t tile = (e == 0 ? beg : end - 1) / stages;
+                const int64_t t0 = tile * stages, t1 = t0 + stages;
+                if ((t0 >= beg && t1 <= end) || (e == 1 && t0 <= beg)) continue;  // whole, or done as the first
+                const int first = p.plan.cta_of(t0), mine = (int)blockIdx.x - first, count = p.plan.cta_of(t1 - 1) - first + 1;
+                if (tid == 64) {
+                    int there = 1;
+                    const uint64_t since = global_ns();
+                    while ((ld_acquire(p.counters + tile) & (kReader - 1)) != stages) {
+                        if (b.abort) { there = 0; break; }
+                        if (global_ns() - since > kWaitLimitNs) {
+                            record_timeout(p.g.status);
+                            b.abort = 1;
+                            there = 0;
+                            break;
+                        }
+                    }
+                    b.last = there;
+                }
+                named_bar_sync(1, 128);
+                if (*(volatile int *)&b.last == 0) break;
+                __threadfence();
+                const int64_t nr = tile % nt * 128 + 4 * lane, m0 = tile / nt * BN;
+                const int cols = (int)std::min<int64_t>(BN, M - m0), c0 = cols * mine / count, c1 = cols * (mine + 1) / count;
+                const int *parts = p.part + tile * p.plan.max_segs * (BN * 128) + 4 * lane;
+                float sw[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) sw[i] = nr + i < N ? bf16_to_f32(ld_nc_u16(p.g.ws + nr + i)) : 0.0f;
+                // a warp adds up one column of 128 rows at a time, 4 rows per lane
+                for (int c = c0 + quarter; c < c1; c += 4 * kColumns) {
+                    int4 v[kColumns];
+#pragma unroll
+                    for (int i = 0; i < kColumns; ++i) v[i] = make_int4(0, 0, 0, 0);
+                    for (int o = 0; o < count; ++o) {
+#pragma unroll
+                        for (int i = 0; i < kColumns; ++i) {
+                            if (c + 4 * i < c1) {
+                                const int4 w = __ldcg(reinterpret_cast<const int4 *>(parts + ((int64_t)o * BN + c + 4 * i) * 128));
+                                v[i].x += w.x; v[i].y += w.y; v[i].z += w.z; v[i].w += w.w;
+                            }
+                        }
+                    }
+#pragma unroll
+                    for (int i = 0; i < kColumns; ++i) {
+                        if (c + 4 * i >= c1) continue;
+                        const int64_t m = m0 + c + 4 * i;
+                        const float sx = __ldg(p.g.xs + m);
+                        const float y0 = __fmul_rn((float)v[i].x, __fmul_rn(sx, sw[0])), y1 = __fmul_rn((float)v[i].y, __fmul_rn(sx, sw[1]));
+                        const float y2 = __fmul_rn((float)v[i].z, __fmul_rn(sx, sw[2])), y3 = __fmul_rn((float)v[i].w, __fmul_rn(sx, sw[3]));
+                        uint16_t *to = p.g.y + m * N + nr;
+                        if (N % 4 == 0) {
+                            if (nr < N) *reinterpret_cast<uint2 *>(to) = make_uint2(pack_bf16x2(y0, y1), pack_bf16x2(y2, y3));
+                        } else {
+                            if (nr < N) to[0] = f32_to_bf16(y0);
+                            if (nr + 1 < N) to[1] = f32_to_bf16(y1);
+                            if (nr + 2 < N) to[2] = f32_to_bf16(y2);
+                            if (nr + 3 < N) to[3] = f32_to_bf16(y3);
+                        }
+                    }
+                }
+                // the last of the tile's readers leaves its counter zero
+                named_bar_sync(1, 128);
+                if (tid == 64 && atomicAdd(p.counters + tile, kReader) / kReader == count - 1) p.counters[tile] = 0;
+            }
+        }
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (wid == 1) tmem_dealloc(tmem, C::kCols);
+}
+
+// SMs of the current device; the kernels' shared-memory limits are raised on their first use there.
 int sms_of_device()
 {
     static std::atomic<int> sms_of[128] = {};
@@ -310,35 +635,137 @@ int sms_of_device()
     int sms = sms_of[dev].load(std::memory_order_acquire);
     if (sms == 0) {
         if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
-        cudaFuncSetAttribute(gemm_i8_pair_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem + 1024);
+        const cudaFuncAttribute limit = cudaFuncAttributeMaxDynamicSharedMemorySize;
+        cudaFuncSetAttribute(gemm_i8_pair_kernel, limit, kSmem + 1024);
+        cudaFuncSetAttribute(gemm_i8_stream_kernel<16>, limit, Stream<16>::kSmem + 1024);
+        cudaFuncSetAttribute(gemm_i8_stream_kernel<32>, limit, Stream<32>::kSmem + 1024);
+        cudaFuncSetAttribute(gemm_i8_stream_kernel<64>, limit, Stream<64>::kSmem + 1024);
+        cudaFuncSetAttribute(gemm_i8_stream_kernel<128>, limit, Stream<128>::kSmem + 1024);
         sms_of[dev].store(sms, std::memory_order_release);
     }
     return sms;
 }
 
-}  // namespace
+int stream_bn(int64_t M) { return M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : 128; }
 
-bool gemm_i8_pair_eligible(int64_t M, int64_t N, int64_t K)
+// Which kernel, and how the stream's units are dealt, by the time that this model gives (microseconds; measured on
+// B200, see the table beside kUnit).
+//   stream, whole tiles: a CTA takes ceil(tiles / SMs) tiles; nothing is added up afterwards
+//   stream, cut: every CTA takes an equal share of the units, 8 at least, and the split tiles cost kCut + M / 16
+//   pairs: ceil(tiles / pairs) tiles of 256 x 256
+// A stage takes kUnit where few CTAs run, and what HBM gives it (kUnitAll with every SM at work); a pair's kPair.
+constexpr double kUnit = 0.27, kUnitAll = 0.40, kCut = 2.0, kPair = 0.29;
+constexpr int kLeastUnits = 8;
+
+struct Choice {
+    bool pairs;
+    Plan plan;  // of the stream
+};
+
+Choice choose(int64_t M, int64_t N, int64_t K, int sms)
 {
-    return M > 128 && N > 128;
+    const int bn = stream_bn(M);
+    Choice c;
+    Plan &p = c.plan;
+    p.nt = (int)((N + 127) / 128);
+    p.tiles = (M + bn - 1) / bn * p.nt;
+    p.stages = (int)((K + kRowBytes - 1) / kRowBytes);
+    p.total = p.tiles * p.stages;
+    const auto unit = [&](int64_t grid) { return std::max(kUnit, kUnitAll * (double)grid / sms); };
+    const int64_t rounds = (p.tiles + sms - 1) / sms, whole_grid = (p.tiles + rounds - 1) / rounds;
+    const double whole = (double)(rounds * p.stages) * unit(whole_grid);
+    const int64_t cut_grid = std::max<int64_t>(1, std::min<int64_t>(sms, p.total / kLeastUnits));
+    const int64_t share = (p.total + cut_grid - 1) / cut_grid;
+    const double cut = (double)share * unit(cut_grid) + kCut + bn / 16;
+    const int64_t pair_tiles = ((M + kTile - 1) / kTile) * ((N + kTile - 1) / kTile);
+    const double pairs = (double)((pair_tiles + sms / 2 - 1) / (sms / 2) * p.stages) * kPair;
+    c.pairs = M > 128 && pairs <= std::min(whole, cut) && pair_tiles < (1 << 30);
+    if (whole <= cut) {
+        p.grid = (int)whole_grid;
+        p.per = (int)(rounds * p.stages);
+        p.extra = 0;
+    } else {
+        p.grid = (int)cut_grid;
+        p.per = (int)(p.total / p.grid);
+        p.extra = (int)(p.total - (int64_t)p.per * p.grid);
+    }
+    p.max_segs = whole <= cut ? 1 : (p.stages + p.per - 1) / p.per + 1;
+    return c;
 }
 
-int launch_gemm_i8_pair(const int8_t *xq, const float *xscales, int64_t M, int64_t N, int64_t K, const int8_t *wq,
-                        const uint16_t *wscales, uint16_t *y, int *status, cudaStream_t st)
+template <int BN>
+int run_stream(const int8_t *xq, const int8_t *wq, const Args &g, const Plan &plan, void *workspace, cudaStream_t st)
 {
+    using C = Stream<BN>;
     CUtensorMap xmap, wmap;
-    if (!encode_tmap_2d(&xmap, CU_TENSOR_MAP_DATA_TYPE_UINT8, xq, (uint64_t)K, (uint64_t)M, (uint64_t)K, kRowBytes, kHalf,
+    if (!encode_tmap_2d(&xmap, CU_TENSOR_MAP_DATA_TYPE_UINT8, xq, (uint64_t)g.K, (uint64_t)g.M, (uint64_t)g.K, kRowBytes, BN,
                         CU_TENSOR_MAP_SWIZZLE_128B) ||
-        !encode_tmap_2d(&wmap, CU_TENSOR_MAP_DATA_TYPE_UINT8, wq, (uint64_t)K, (uint64_t)N, (uint64_t)K, kRowBytes, kHalf,
+        !encode_tmap_2d(&wmap, CU_TENSOR_MAP_DATA_TYPE_UINT8, wq, (uint64_t)g.K, (uint64_t)g.N, (uint64_t)g.K, kRowBytes, 128,
                         CU_TENSOR_MAP_SWIZZLE_128B))
         return -1;
-    const int sms = sms_of_device();
-    if (sms < 2) return -2;
-    Args a{M, N, K, xscales, wscales, y, status, (int)((M + kTile - 1) / kTile), (int)((N + kTile - 1) / kTile), 0};
-    a.band = (int)std::max<int64_t>(1, std::min<int64_t>(a.mt, kBandBytes / (kTile * K)));
+    StreamArgs a{g, plan, nullptr, nullptr};
+    uint8_t *w8 = static_cast<uint8_t *>(workspace);
+    a.counters = reinterpret_cast<int *>(w8);
+    a.part = reinterpret_cast<int *>(w8 + counter_region_bytes(a.plan.tiles));
+    if (plan.max_segs > 1 && clear_extra_counters(workspace, plan.tiles, st) != cudaSuccess) return -2;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)a.plan.grid);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = C::kSmem + 1024;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    cudaLaunchKernelEx(&cfg, gemm_i8_stream_kernel<BN>, xmap, wmap, a);  // a failure is the caller's last error
+    return 0;
+}
+
+int run_pairs(const int8_t *xq, const int8_t *wq, Args a, int sms, cudaStream_t st)
+{
+    CUtensorMap xmap, wmap;
+    if (!encode_tmap_2d(&xmap, CU_TENSOR_MAP_DATA_TYPE_UINT8, xq, (uint64_t)a.K, (uint64_t)a.M, (uint64_t)a.K, kRowBytes, kHalf,
+                        CU_TENSOR_MAP_SWIZZLE_128B) ||
+        !encode_tmap_2d(&wmap, CU_TENSOR_MAP_DATA_TYPE_UINT8, wq, (uint64_t)a.K, (uint64_t)a.N, (uint64_t)a.K, kRowBytes, kHalf,
+                        CU_TENSOR_MAP_SWIZZLE_128B))
+        return -1;
+    a.mt = (int)((a.M + kTile - 1) / kTile);
+    a.nt = (int)((a.N + kTile - 1) / kTile);
+    a.band = (int)std::max<int64_t>(1, std::min<int64_t>(a.mt, kBandBytes / (kTile * a.K)));
     const int64_t pairs = std::min<int64_t>((int64_t)a.mt * a.nt, sms / 2);
     gemm_i8_pair_kernel<<<(unsigned)(2 * pairs), kThreads, kSmem + 1024, st>>>(xmap, wmap, a);
     return 0;
+}
+
+}  // namespace
+
+size_t gemm_int8_workspace_bytes(int64_t M, int64_t N, int64_t K)
+{
+    if (M <= 0 || N <= 0 || K <= 0 || K % 32 != 0) return 0;
+    int dev = 0, sms = 148;
+    cudaGetDevice(&dev);
+    cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    const Choice c = choose(M, N, K, sms);
+    if (c.pairs || c.plan.max_segs == 1) return 0;  // no tile is split
+    return counter_region_bytes(c.plan.tiles) +
+           ((size_t)c.plan.tiles * c.plan.max_segs * stream_bn(M) * 128 * sizeof(int) + 255) / 256 * 256;
+}
+
+int launch_gemm_w8a8_int8(const int8_t *xq, const float *xscales, int64_t M, int64_t N, int64_t K, const int8_t *wq,
+                          const uint16_t *wscales, uint16_t *y, void *workspace, int *status, cudaStream_t st)
+{
+    const int sms = sms_of_device();
+    if (sms < 2) return -2;
+    const Args g{M, N, K, xscales, wscales, y, status, 0, 0, 0};
+    const Choice c = choose(M, N, K, sms);
+    if (c.pairs) return run_pairs(xq, wq, g, sms, st);
+    switch (stream_bn(M)) {
+    case 16: return run_stream<16>(xq, wq, g, c.plan, workspace, st);
+    case 32: return run_stream<32>(xq, wq, g, c.plan, workspace, st);
+    case 64: return run_stream<64>(xq, wq, g, c.plan, workspace, st);
+    default: return run_stream<128>(xq, wq, g, c.plan, workspace, st);
+    }
 }
 
 }  // namespace wq

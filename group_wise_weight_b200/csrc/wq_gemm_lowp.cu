@@ -72,7 +72,7 @@ constexpr int kThreads = 192;   // warp 0: copies, warp 1: MMA, warps 2..5: epil
 constexpr int kEpiWarp0 = 2;
 constexpr int kSfAtom = 512;    // block scales of 128 rows x 64 values of K
 
-enum Kind { kFp8 = 0, kNvfp4 = 1, kInt8 = 2 };
+enum Kind { kFp8 = 0, kNvfp4 = 1 };
 
 template <int BN, int KIND>
 struct Cfg {
@@ -88,7 +88,7 @@ struct Cfg {
     // two accumulators of BN columns, then (NVFP4) 16 columns of weight block scales and 16 of activation
     static constexpr uint32_t kSfaCol = 2 * BN, kSfbCol = 2 * BN + 16;
     static constexpr uint32_t kTmemCols = KIND == kNvfp4 ? 512 : 2 * BN;
-    static_assert(KIND != kNvfp4 || BN == 128, "NVFP4 tiles are 128 x 128");
+    static_assert(KIND == kFp8 || BN == 128, "NVFP4 tiles are 128 x 128");
     static_assert((kStageBytes & 1023) == 0, "stages stay 1024-byte aligned (128-byte swizzle atoms)");
 };
 
@@ -120,16 +120,6 @@ __device__ __forceinline__ void mma_f8(uint32_t d_tmem, uint64_t a_desc, uint64_
                  : "memory");
 }
 
-// The same for kind::i8: signed bytes, exact 32-bit integer accumulation.
-__device__ __forceinline__ void mma_i8(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
-                                       uint32_t accumulate)
-{
-    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-                 "tcgen05.mma.cta_group::1.kind::i8 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-                 "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
-                 : "memory");
-}
-
 // D[tmem] (+)= (A * SFA) (B * SFB)^T, kind::mxf4nvf4 with one E4M3 scale per 16 values of K.
 __device__ __forceinline__ void mma_nvf4(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
                                          uint32_t sfa_tmem, uint32_t sfb_tmem, uint32_t accumulate)
@@ -151,12 +141,6 @@ __device__ __forceinline__ void sf_copy(uint32_t taddr, uint64_t s_desc)
 __host__ __device__ constexpr uint32_t idesc_e4m3_f32(int m, int n)
 {
     return (1u << 4) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(m >> 4) << 24);
-}
-
-// Instruction descriptor, kind::i8: signed A and B (format code 1), both K-major, s32 D (format code 2), M x N.
-__host__ __device__ constexpr uint32_t idesc_s8_s32(int m, int n)
-{
-    return (2u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(m >> 4) << 24);
 }
 
 // Block-scaled instruction descriptor, kind::mxf4nvf4: E2M1 A and B (format code 1), both K-major, E4M3
@@ -182,13 +166,11 @@ __device__ __forceinline__ void wait_drain(uint64_t *bar, uint32_t parity, int *
 
 // Operands of one call.  For FP8: xs = per-tensor activation scale, ws = per-row weight scales (stride 1).
 // For NVFP4: xs, ws = the two tensor scales (ws stride 0); sfw, sfx = block scales in the atom layout.
-// For INT8: xs = per-row activation scales, ws16 = per-row weight scales in bf16; the partial sums are integers.
 struct Args {
     int64_t M, N, K;
     const float *xs, *ws;
     int ws_stride;
     const uint8_t *sfw, *sfx;
-    const uint16_t *ws16;
     uint16_t *y;
     float *part;
     int *counters;
@@ -219,7 +201,7 @@ gemm_lowp_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant
     Sched sc;
     sc.n_tiles = (N + kTileN - 1) / kTileN;
     sc.tiles = sc.n_tiles * ((M + BN - 1) / BN);
-    sc.spt = ((KIND == kNvfp4 ? p.K / 2 : p.K) + kRowBytes - 1) / kRowBytes;
+    sc.spt = (KIND == kNvfp4 ? p.K / 2 : p.K) / kRowBytes;
     sc.total = sc.tiles * sc.spt;
     sc.per = sc.total / gridDim.x;
     sc.extra = sc.total % gridDim.x;
@@ -279,8 +261,7 @@ gemm_lowp_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant
     } else if (wid == 1) {
         // ------------------------------ MMA issuer (one lane) ------------------------------
         if (lane == 0) {
-            constexpr uint32_t idesc = KIND == kNvfp4 ? idesc_nvf4(kTileN, BN)
-                                       : KIND == kInt8 ? idesc_s8_s32(kTileN, BN) : idesc_e4m3_f32(kTileN, BN);
+            constexpr uint32_t idesc = KIND == kNvfp4 ? idesc_nvf4(kTileN, BN) : idesc_e4m3_f32(kTileN, BN);
             Ring fr, dr;
             int seg = 0;
             const uint32_t base = smem_u32(smem);
@@ -309,11 +290,6 @@ gemm_lowp_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant
                             mma_nvf4(d_col, smem_desc(a + 32u * j, 16, 1024, 2), smem_desc(b + 32u * j, 16, 1024, 2),
                                      idesc, tmem + C::kSfaCol + 4u * j, tmem + C::kSfbCol + 4u * j,
                                      (ks > ks0 || j > 0) ? 1u : 0u);
-                    } else if (KIND == kInt8) {
-#pragma unroll
-                        for (int j = 0; j < 4; ++j)
-                            mma_i8(d_col, smem_desc(a + 32u * j, 16, 1024, 2), smem_desc(b + 32u * j, 16, 1024, 2),
-                                   idesc, (ks > ks0 || j > 0) ? 1u : 0u);
                     } else {
 #pragma unroll
                         for (int j = 0; j < 4; ++j)
@@ -336,7 +312,7 @@ gemm_lowp_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant
         const int quarter = wid & 3;
         const int r = quarter * 32 + lane;  // row of the tile = tensor-memory lane
         const uint32_t lane_bits = (uint32_t)(quarter * 32) << 16;
-        const float xs = KIND == kInt8 ? 0.0f : *p.xs;
+        const float xs = *p.xs;
         Ring dr;
         for (int64_t u = beg; u < end;) {
             const int64_t tile = u / spt;
@@ -347,12 +323,7 @@ gemm_lowp_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant
             const int64_t m0 = mt * BN;
             mbar_wait_fast(&d_full[dr.slot], dr.phase, status, abort_flag);
             tc_fence_after();
-            const float scale = n >= N ? 0.0f : KIND == kInt8 ? bf16_to_f32(p.ws16[n]) : xs * p.ws[n * p.ws_stride];
-            // y of accumulator column m (INT8: the integer converted to binary32, times the product of the scales)
-            auto result = [&](uint32_t bits, int64_t m) {
-                return KIND == kInt8 ? f32_to_bf16(__fmul_rn((float)(int)bits, __fmul_rn(__ldg(p.xs + m), scale)))
-                                     : f32_to_bf16(__uint_as_float(bits) * scale);
-            };
+            const float scale = n < N ? xs * p.ws[n * p.ws_stride] : 0.0f;
             const uint32_t d_addr = tmem + lane_bits + dr.slot * (uint32_t)BN;
             if (ks0 == 0 && ks1 == spt) {
 #pragma unroll 1
@@ -363,7 +334,7 @@ gemm_lowp_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant
                     if (n < N) {
 #pragma unroll
                         for (int c = 0; c < 32; ++c)
-                            if (m0 + c0 + c < M) p.y[(m0 + c0 + c) * N + n] = result(v[c], m0 + c0 + c);
+                            if (m0 + c0 + c < M) p.y[(m0 + c0 + c) * N + n] = f32_to_bf16(__uint_as_float(v[c]) * scale);
                     }
                 }
             } else {
@@ -413,23 +384,20 @@ gemm_lowp_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant
                         uint32_t v[32];
                         tmem_ld32(d_addr + (uint32_t)c0, v);
                         tmem_wait_ld();
-                        uint32_t tot[32];
+                        float tot[32];
 #pragma unroll
-                        for (int c = 0; c < 32; ++c) tot[c] = 0u;
+                        for (int c = 0; c < 32; ++c) tot[c] = 0.0f;
                         for (int64_t o = 0; o < nseg; ++o) {
                             const float *other = p.part + ((tile * p.max_segs + o) * BN) * kTileN;
 #pragma unroll
-                            for (int c = 0; c < 32; ++c) {
-                                const float part = (o == my_seg) ? __uint_as_float(v[c])
-                                                                 : __ldcg(other + (int64_t)(c0 + c) * kTileN + r);
-                                tot[c] = KIND == kInt8 ? tot[c] + __float_as_uint(part)
-                                                       : __float_as_uint(__uint_as_float(tot[c]) + part);
-                            }
+                            for (int c = 0; c < 32; ++c)
+                                tot[c] += (o == my_seg) ? __uint_as_float(v[c])
+                                                        : __ldcg(other + (int64_t)(c0 + c) * kTileN + r);
                         }
                         if (n < N) {
 #pragma unroll
                             for (int c = 0; c < 32; ++c)
-                                if (m0 + c0 + c < M) p.y[(m0 + c0 + c) * N + n] = result(tot[c], m0 + c0 + c);
+                                if (m0 + c0 + c < M) p.y[(m0 + c0 + c) * N + n] = f32_to_bf16(tot[c] * scale);
                         }
                     }
                     named_bar_sync(1, 128);
@@ -469,10 +437,6 @@ int sms_of_device()
         cudaFuncSetAttribute(gemm_lowp_kernel<64, kFp8>, cudaFuncAttributeMaxDynamicSharedMemorySize, optin);
         cudaFuncSetAttribute(gemm_lowp_kernel<128, kFp8>, cudaFuncAttributeMaxDynamicSharedMemorySize, optin);
         cudaFuncSetAttribute(gemm_lowp_kernel<256, kFp8>, cudaFuncAttributeMaxDynamicSharedMemorySize, optin);
-        cudaFuncSetAttribute(gemm_lowp_kernel<32, kInt8>, cudaFuncAttributeMaxDynamicSharedMemorySize, optin);
-        cudaFuncSetAttribute(gemm_lowp_kernel<64, kInt8>, cudaFuncAttributeMaxDynamicSharedMemorySize, optin);
-        cudaFuncSetAttribute(gemm_lowp_kernel<128, kInt8>, cudaFuncAttributeMaxDynamicSharedMemorySize, optin);
-        cudaFuncSetAttribute(gemm_lowp_kernel<256, kInt8>, cudaFuncAttributeMaxDynamicSharedMemorySize, optin);
         cudaFuncSetAttribute(gemm_lowp_kernel<128, kNvfp4>, cudaFuncAttributeMaxDynamicSharedMemorySize, optin);
         it = sms_of.emplace(dev, v).first;
     }
@@ -488,7 +452,7 @@ Plan plan(int64_t M, int64_t N, int64_t kbytes, int bn, int sms)
 {
     Plan p;
     p.tiles = ((N + kTileN - 1) / kTileN) * ((M + bn - 1) / bn);
-    p.spt = (kbytes + kRowBytes - 1) / kRowBytes;
+    p.spt = kbytes / kRowBytes;
     p.total = p.tiles * p.spt;
     p.grid = std::max<int64_t>(1, std::min<int64_t>(p.total, sms));
     const int64_t per = p.total / p.grid;  // >= 1
@@ -554,29 +518,6 @@ int launch_gemm_w8a8_fp8(const uint8_t *xq, const float *xscale, int64_t M, int6
     case 64: return run<64, kFp8>(xq, wq, a, workspace, st);
     case 128: return run<128, kFp8>(xq, wq, a, workspace, st);
     default: return run<256, kFp8>(xq, wq, a, workspace, st);
-    }
-}
-
-size_t gemm_int8_workspace_bytes(int64_t M, int64_t N, int64_t K)
-{
-    if (M <= 0 || N <= 0 || K <= 0 || K % 32 != 0) return 0;
-    return workspace_bytes(M, N, K, fp8_bn(M));
-}
-
-int launch_gemm_w8a8_int8(const int8_t *xq, const float *xscales, int64_t M, int64_t N, int64_t K, const int8_t *wq,
-                          const uint16_t *wscales, uint16_t *y, void *workspace, int *status, cudaStream_t st)
-{
-    Args a{};
-    a.M = M; a.N = N; a.K = K;
-    a.xs = xscales; a.ws16 = wscales;
-    a.y = y; a.status = status;
-    if (gemm_i8_pair_eligible(M, N, K)) return launch_gemm_i8_pair(xq, xscales, M, N, K, wq, wscales, y, status, st);
-    const uint8_t *x = reinterpret_cast<const uint8_t *>(xq), *w = reinterpret_cast<const uint8_t *>(wq);
-    switch (fp8_bn(M)) {
-    case 32: return run<32, kInt8>(x, w, a, workspace, st);
-    case 64: return run<64, kInt8>(x, w, a, workspace, st);
-    case 128: return run<128, kInt8>(x, w, a, workspace, st);
-    default: return run<256, kInt8>(x, w, a, workspace, st);
     }
 }
 

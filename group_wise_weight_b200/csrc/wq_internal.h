@@ -167,16 +167,12 @@ int launch_kv_attn(bool fp8, const uint16_t *q, const uint8_t *kc, const uint16_
 void launch_quantize_int8_tokens(const void *x, int xtype, int64_t M, int64_t K, int64_t ldx, int8_t *q, float *s,
                                  cudaStream_t st);
 
-// INT8 W8A8 tcgen05 matmul (wq_gemm_lowp.cu): K % 32 == 0, K < 131072.  Workspace as the FP8 matmul's, with
-// 32-bit integer partials.  Returns 0, or -1 if a tensor map cannot be encoded, -2 if a clear fails.
+// INT8 W8A8 tcgen05 matmul (wq_gemm_i8.cu): K % 32 == 0, K < 131072.  Workspace as the FP8 matmul's (counters first),
+// with 32-bit integer parts; none for many rows.  Returns 0, or -1 if a tensor map cannot be encoded, -2 if a clear
+// or a query of the device fails.
 size_t gemm_int8_workspace_bytes(int64_t M, int64_t N, int64_t K);
 int launch_gemm_w8a8_int8(const int8_t *xq, const float *xscales, int64_t M, int64_t N, int64_t K, const int8_t *wq,
                           const uint16_t *wscales, uint16_t *y, void *workspace, int *status, cudaStream_t st);
-
-// The same on pairs of SMs (wq_gemm_i8.cu), for many rows: no workspace.
-bool gemm_i8_pair_eligible(int64_t M, int64_t N, int64_t K);
-int launch_gemm_i8_pair(const int8_t *xq, const float *xscales, int64_t M, int64_t N, int64_t K, const int8_t *wq,
-                        const uint16_t *wscales, uint16_t *y, int *status, cudaStream_t st);
 
 // Per-head norms and rotary positions of queries and keys (wq_rope.cu): D in {64, 128}, rot a multiple of 16.
 // qw, kw: both null for positions alone.

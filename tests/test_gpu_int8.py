@@ -176,8 +176,10 @@ def test_matmul_refusals():
                       ((xq, xs.cpu(), w, ws), TypeError)):
         with pytest.raises(err):
             wq.wq_gemm_w8a8_int8(*args)
+    args = [t.cuda() for t in operands(1, 2048, 8192, 1)]
+    assert wq.wq_gemm_w8a8_int8_workspace_bytes(1, 2048, 8192) > 0
     with pytest.raises(wq.WQError):
-        wq.wq_gemm_w8a8_int8(xq, xs, w, ws, workspace=torch.zeros(16, dtype=torch.uint8).cuda())
+        wq.wq_gemm_w8a8_int8(*args, workspace=torch.zeros(16, dtype=torch.uint8).cuda())
 
 
 def test_quantised_linear_against_the_full_precision_product():
