@@ -13,15 +13,17 @@
 //
 // Few rows (gemm_i8_stream_kernel): the weights are read once and bound the
 // call, so the work is cut along K as well: units of (tile, stage) in tile
-// order, dealt evenly over the SMs.  A tile is 128 or 256 weight rows (the
-// MMA's M, so a token costs one of its N columns) by 16 to 128 tokens; 256
-// weight rows where the tokens' own bytes would weigh on L2.  A CTA
-// that holds part of a tile leaves its integer sums in the workspace and adds
-// its stages to the tile's counter; the one that completes the counter adds
-// the parts up (exact, so in any order) and writes y.  Nobody waits for
-// anybody.  The kernel is launched to overlap the previous one's end: before
-// that has completed it only asks L2 to fetch its first weights (a hint; no
-// value read).
+// order, dealt evenly over the SMs, or whole tiles where that is quicker.  A
+// tile is 128 weight rows (the MMA's M, so a token costs one of its N columns)
+// by 16 to 128 tokens.  A CTA that holds part of a tile leaves its integer
+// sums in the workspace and adds its stages to the tile's counter.  With few
+// parts and tokens the one that completes the counter adds the parts up
+// (exact, so in any order) and writes y; with more, every CTA of the tile
+// comes back at the end of its units, waits for the counter (bounded: the
+// parts of others never wait for this) and does a share of the columns.  The
+// kernel is launched to overlap the previous one's end: before that has
+// completed it only asks L2 to fetch its first weights (a hint; no value
+// read).
 //
 // Many rows (gemm_i8_pair_kernel): the tensor cores bound the product, provided
 // the operands reach them: at 8,192 int8 multiply-adds per cycle an SM that
@@ -339,12 +341,11 @@ struct Stream {
     static constexpr int kStages = BN == 16 ? 6 : BN == 32 ? 5 : BN == 64 ? 8 : 6;
     static constexpr int kBarOff = kStages * kStage;
     static constexpr int kSmem = kBarOff + 256;
-    static constexpr bool kSliced = BN >= 64;  // who adds up a split tile: its CTAs, a share each, or the last to finish
     static constexpr uint32_t kCols = 2 * BN;  // two accumulators
 };
 
 constexpr int kReader = 1 << 20;  // a counter's unit for CTAs that have read their share (the stages stay below it)
-constexpr int kColumns = 4;       // columns in flight per warp of the sliced sum
+constexpr int kColumns = 4;       // columns in flight per warp of the shared sum
 
 // Device-scope load with acquire semantics: later reads see what was written before the matching add.
 __device__ __forceinline__ int ld_acquire(const int *p)
@@ -365,6 +366,7 @@ static_assert(sizeof(StreamBars) <= 256, "the barrier area");
 struct Plan {
     int64_t tiles, total;
     int nt, stages, grid, per, extra, max_segs;
+    bool shared;  // who adds up a split tile: its CTAs, a share of the columns each, or the last of them to finish
     __host__ __device__ int64_t begin_of(int b) const
     {
         const int64_t u = (int64_t)b * per + (b < extra ? b : extra);
@@ -499,7 +501,7 @@ gemm_i8_stream_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_con
             int *parts = p.part + tile * p.plan.max_segs * (BN * 128);
             const int first = p.plan.cta_of(tile * stages), mine = (int)blockIdx.x - first;
             const int count = whole ? 1 : p.plan.cta_of(tile * stages + stages - 1) - first + 1;
-            bool writes = whole;  // sliced tiles are written below
+            bool writes = whole;  // shared tiles are written below
             if (!whole) {
 #pragma unroll 1
                 for (int c = 0; c < cols; c += 16) {
@@ -513,7 +515,7 @@ gemm_i8_stream_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_con
                 }
                 __threadfence();
                 named_bar_sync(1, 128);
-                if (C::kSliced) {
+                if (p.plan.shared) {
                     if (tid == 64) atomicAdd(p.counters + tile, s1 - s0);
                 } else {
                     if (tid == 64) b.last = atomicAdd(p.counters + tile, s1 - s0) + (s1 - s0) == stages;
@@ -551,7 +553,7 @@ gemm_i8_stream_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_con
             if (lane == 0) mbar_arrive(&b.d_empty[n & 1u]);
             u += s1 - s0;
         }
-        if (C::kSliced && ok) {
+        if (p.plan.shared && ok) {
             // the split tiles, first and last of this CTA's range: its share of their columns
             for (int e = 0; e < 2; ++e) {
                 const int64_t tile = (e == 0 ? beg : end - 1) / stages;
@@ -648,8 +650,10 @@ int sms_of_device()
 
 int stream_bn(int64_t M) { return M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : 128; }
 
-// Which kernel, and how the stream's units are dealt, by the time that this model gives (microseconds; measured on
-// B200, see the table beside kUnit).
+// Which kernel, and how the stream's units are dealt, by the time that this model gives (microseconds).  On B200 it
+// chooses, with the other choice's time behind: M = 1, 10240 x 8192: cut 21.2 (whole 28); M = 100, 10240 x 8192: whole
+// 26.7 (cut 31.7); M = 100, 28672 x 1024: whole 15.8 (cut 26.5); M = 100, 8192 x 28672: cut 57 (pairs 72); M = 256, 8192 x
+// 8192: pairs 27 (cut 47); M = 192, 128 x 28672: cut 17 (pairs 65).
 //   stream, whole tiles: a CTA takes ceil(tiles / SMs) tiles; nothing is added up afterwards
 //   stream, cut: every CTA takes an equal share of the units, 8 at least, and the split tiles cost kCut + M / 16
 //   pairs: ceil(tiles / pairs) tiles of 256 x 256
@@ -690,6 +694,9 @@ Choice choose(int64_t M, int64_t N, int64_t K, int sms)
         p.extra = (int)(p.total - (int64_t)p.per * p.grid);
     }
     p.max_segs = whole <= cut ? 1 : (p.stages + p.per - 1) / p.per + 1;
+    // sharing costs a wait for the other CTAs (K = N = 8192, up to 4 parts a tile: M = 4 17.0 us without, 19.6 with), adding
+    // up alone costs by parts and columns (N = 128, K = 28672, 29 parts: M = 16 26.8 us alone, 13.9 shared)
+    p.shared = bn > 16 || p.max_segs * (M + 4) >= 72;
     return c;
 }
 
