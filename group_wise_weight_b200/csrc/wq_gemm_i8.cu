@@ -21,9 +21,11 @@
 // (exact, so in any order) and writes y; with more, every CTA of the tile
 // comes back at the end of its units, waits for the counter (bounded: the
 // parts of others never wait for this) and does a share of the columns.  The
-// kernel is launched to overlap the previous one's end: before that has
-// completed it only asks L2 to fetch its first weights (a hint; no value
-// read).
+// ring takes 200 KB: what an SM has in flight sets the rate (M = 1, N = 57344,
+// K = 8192: 6 stages of 18 KB 81.6 us, 11 stages 72.8 us, 6.45 TB/s).  The kernel
+// is launched to set up while the previous one ends (0.4 us of a call; asking
+// L2 for its first weights then gained nothing) and reads and writes nothing
+// before that has completed.
 //
 // Many rows (gemm_i8_pair_kernel): the tensor cores bound the product, provided
 // the operands reach them: at 8,192 int8 multiply-adds per cycle an SM that
@@ -329,16 +331,11 @@ __device__ __forceinline__ void mma_one(uint32_t d_tmem, uint64_t a_desc, uint64
                  : "memory");
 }
 
-__device__ __forceinline__ void prefetch_l2(const CUtensorMap *map, int x, int y)
-{
-    asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global [%0, {%1, %2}];" ::"l"(map), "r"(x), "r"(y) : "memory");
-}
-
-// BN tokens by 128 weight rows.  The narrow tiles leave room for the next call's CTA beside this one.
+// BN tokens by 128 weight rows.
 template <int BN>
 struct Stream {
     static constexpr int kStage = kOperand + BN * kRowBytes;
-    static constexpr int kStages = BN == 16 ? 6 : BN == 32 ? 5 : BN == 64 ? 8 : 6;
+    static constexpr int kStages = 200 * 1024 / kStage;  // 11, 10, 8, 6
     static constexpr int kBarOff = kStages * kStage;
     static constexpr int kSmem = kBarOff + 256;
     static constexpr uint32_t kCols = 2 * BN;  // two accumulators
@@ -356,7 +353,7 @@ __device__ __forceinline__ int ld_acquire(const int *p)
 }
 
 struct StreamBars {
-    uint64_t full[8], empty[8], d_full[2], d_empty[2], done;
+    uint64_t full[11], empty[11], d_full[2], d_empty[2], done;
     int abort, last;
     uint32_t tmem;
 };
@@ -411,11 +408,6 @@ gemm_i8_stream_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_con
         mbar_init(&b.done, 1);
         b.abort = 0;
         fence_mbar_init();
-    }
-    if (wid == 0 && lane < (int)S && beg + lane < end) {
-        const int64_t tile = (beg + lane) / stages;
-        const int s = (int)(beg + lane - tile * stages);
-        prefetch_l2(&wmap, s * kRowBytes, (int)(tile % nt) * 128);
     }
     if (wid == 1) tmem_alloc(&b.tmem, C::kCols);
     tc_fence_before();
