@@ -20,8 +20,10 @@
 // The r = Hq / H query heads of a KV head share its keys and values: a tile's
 // 128 rows are (token, head) pairs, token-major, so it covers 128 / r tokens
 // and short sequences still fill it.  A work item is two such tiles
-// (consecutive tokens) of one KV head; a persistent CTA per SM takes items,
-// the longest first.
+// (consecutive tokens) of one KV head.  The grid has a CTA per item; one that
+// runs claims further ones before they are launched (cluster launch control)
+// and does their items too, so an SM keeps its pipeline filled across items of
+// any length.
 //
 // Per block of 128 keys and tile: S = Q K^T (both operands K-major in shared
 // memory, loaded by TMA with the 128-byte swizzle) into 128 columns of tensor
@@ -33,9 +35,9 @@
 // of the tensor core per tile and its 16,384 exponentials as many of the
 // special-function units, so both are at their limits together.
 //
-// Roles (384 threads, two warps idle): warps 0-3 and 4-7 the two softmax
-// warpgroups, warp 8 the copies (Q of the next item as soon as its tile is
-// free, a ring of K and V blocks), warp 9 the MMAs.
+// Roles (512 threads): warps 0-3 and 4-7 the two softmax warpgroups, warp 8 the
+// items and a ring of K and V blocks, one thread of warp 9 the MMAs, warps 10
+// and 11 a tile's Q each (the next item's as soon as the tile is free), warps 12-15 the outputs: O / l in bf16 while the tile's warpgroup is at the next item.
 // Keys past a tile's last visible one are left out of both products in steps
 // of 16; inside the step their p is 0, and the copy warp zeroes the V rows past
 // the sequence's end, so what lies behind a sequence never enters a sum.
@@ -52,8 +54,9 @@ namespace {
 
 constexpr int kRows = 128;      // (token, head) rows per tile
 constexpr int kKeys = 128;      // keys per block
-constexpr int kThreads = 384;
-constexpr int kLoadWarp = 8, kMmaWarp = 9;
+constexpr int kThreads = 512;
+constexpr int kLoadWarp = 8, kMmaWarp = 9, kQueryWarp = 10, kOutWarp = 12;
+constexpr int kSoftmaxRegs = 184, kOtherRegs = 72;  // 256 threads each, of 128 at launch
 constexpr int kPart = 64, kParts = kKeys / kPart;  // keys of P that are handed to the tensor core at a time
 constexpr uint32_t kTmemCols = 512;
 constexpr float kSlack = 8.0f;  // log2 of the growth of p that is let pass before m moves
@@ -63,11 +66,16 @@ struct Cfg {
     static constexpr int kCols = D / 64;               // 128-byte column blocks of a row
     static constexpr int kBlkBytes = kRows * 128;      // one column block of 128 rows
     static constexpr int kTileBytes = kCols * kBlkBytes;
+    // columns of tensor memory: S of tile x at 128 x, O at 256 + D x, P over S, or (where O leaves room) behind O, so
+    // that S can be overwritten as soon as it is in registers
+    static constexpr bool kOwnP = D == 64;
+    static constexpr uint32_t kPCol = kOwnP ? 384 : 0, kPStride = kOwnP ? 64 : 128;
     static constexpr int kStages = D == 128 ? 4 : 8;   // K and V blocks in the ring
     static constexpr int kRing = 2 * kTileBytes;       // after the two Q tiles
-    static constexpr int kOutOff = kRing + kStages * kTileBytes;  // 32 rows of 32 output values per softmax warp
-    static constexpr int kBarOff = kOutOff + 8 * 32 * 64;
-    static constexpr int kBytes = kBarOff + 512;
+    static constexpr int kOutOff = kRing + kStages * kTileBytes;  // 32 rows of 32 output values per output warp
+    static constexpr int kScaleOff = kOutOff + 4 * 32 * 64;        // 1 / l of two items' rows, per tile
+    static constexpr int kBarOff = kScaleOff + 4 * kRows * 4;
+    static constexpr int kBytes = kBarOff + 640;
 };
 
 struct PromptArgs {
@@ -89,16 +97,24 @@ struct Item {
     {
         return tok0 + x * tpt < len ? (last(x, tpt) + kKeys - 1) / kKeys : 0;
     }
+    // block j holds the sequence's end within a step of 16 keys: its first row past the end, or 0
+    __device__ __forceinline__ int tail(int j) const
+    {
+        const int rows = len - j * kKeys;
+        return rows < kKeys && (rows & 15) ? rows : 0;
+    }
 };
 
 struct Bars {
     uint64_t kv_full[8], kv_empty[8], q_full[2], q_empty[2], s_full[2], p_full[2][kParts], pv_done[2], item_full[2],
-        item_empty[2], tail, done;
+        item_empty[2], landed[8], done, claim,
+        l_full[2][2], o_free[2], s_free[2];
+    __align__(16) uint8_t claimed[16];
     Item items[2];
     int abort, pad;
     uint32_t tmem;
 };
-static_assert(sizeof(Bars) <= 512, "the barrier area");
+static_assert(sizeof(Bars) <= 640, "the barrier area");
 
 // Pairs of tiles of the packed batch in order; the one with index `t`: its sequence's first row and length and its
 // first token.  Whole warp; returns the number of pairs seen up to and including its sequence's, and sets `found`.
@@ -155,6 +171,11 @@ __device__ __forceinline__ f32x2 add2_pairs(f32x2 a, f32x2 b)
     return r;
 }
 
+template <int N>
+__device__ __forceinline__ void registers_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
+template <int N>
+__device__ __forceinline__ void registers_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
+
 // One lane of the (whole) warp.
 __device__ __forceinline__ bool elect_one()
 {
@@ -168,6 +189,37 @@ __device__ __forceinline__ float max3(float a, float b, float c)
     float d;
     asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
     return d;
+}
+
+// Asks the hardware for a CTA of the grid that has not been launched, to do its items here (the answer arrives on `bar`).
+__device__ __forceinline__ void claim_cta(uint8_t *answer, uint64_t *bar)
+{
+    mbar_arrive_expect_tx(bar, 16);
+    asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];"
+                 ::"r"(smem_u32(answer)), "r"(smem_u32(bar))
+                 : "memory");
+}
+
+// The claimed CTA's blockIdx.x, or -1 when none was left.
+__device__ __forceinline__ int claimed_cta(const uint8_t *answer)
+{
+    uint32_t x, got;
+    asm volatile("{\n\t.reg .pred p;\n\t.reg .b128 r;\n\tld.shared.b128 r, [%2];\n\t"
+                 "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, r;\n\t"
+                 "selp.u32 %1, 1, 0, p;\n\tmov.u32 %0, 0;\n\t"
+                 "@p clusterlaunchcontrol.query_cancel.get_first_ctaid.v4.b32.b128 {%0, _, _, _}, r;\n\t}"
+                 : "=r"(x), "=r"(got)
+                 : "r"(smem_u32(answer))
+                 : "memory");
+    return got ? (int)x : -1;
+}
+
+// Waits whatever `abort` says: for copies and MMAs that must be over before the CTA may end.
+__device__ __forceinline__ void drain(uint64_t *bar, uint32_t parity, int *status)
+{
+    const uint64_t since = global_ns();
+    while (!mbar_try_wait(bar, parity))
+        if (global_ns() - since > kWaitLimitNs) { record_timeout(status); return; }
 }
 
 struct Wait {
@@ -208,10 +260,14 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_consta
             for (int c = 0; c < kParts; ++c) mbar_init(&b.p_full[i][c], 4);
             mbar_init(&b.pv_done[i], 1);
             mbar_init(&b.item_full[i], 1);
-            mbar_init(&b.item_empty[i], 9);  // 8 softmax warps and the MMA warp
+            mbar_init(&b.item_empty[i], 15);  // 8 softmax, 4 output and 2 Q warps, the MMA thread
+            mbar_init(&b.s_free[i], 4);
+            for (int c = 0; c < 2; ++c) mbar_init(&b.l_full[i][c], 4);
+            mbar_init(&b.o_free[i], 4);
         }
         mbar_init(&b.done, 1);
-        mbar_init(&b.tail, 1);
+        mbar_init(&b.claim, 1);
+        for (uint32_t i = 0; i < S; ++i) mbar_init(&b.landed[i], 1);
         b.abort = 0;
         fence_mbar_init();
     }
@@ -219,28 +275,43 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_consta
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = b.tmem;  // S of tile x at 128 x, O of tile x at 256 + D x
+    const uint32_t tmem = b.tmem;
 
     // 384 threads of 168 registers at launch: 200 for the softmax warpgroups, 104 for the third
 
     if (wid == kLoadWarp) {
         // ------------------------------ items and copies ------------------------------
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
+        registers_dec<kOtherRegs>();
         Item it{};
         int64_t pairs;
         locate(p, -1, it, pairs);
         const int64_t total = pairs * p.H;
-        uint32_t slot = 0, phase = 0, loads = 0, nitem = 0, tails = 0, qn[2] = {0, 0};
+        uint32_t slot = 0, phase = 0, loads = 0, nitem = 0;
         bool ok = true;
-        for (int64_t i = blockIdx.x;; i += gridDim.x) {
+        uint32_t claims = 0;
+        int64_t cta = blockIdx.x, i = cta;
+        if (lane == 0) claim_cta(b.claimed, &b.claim);
+        for (;;) {
+            // this CTA's items, then those of CTAs claimed from the grid (the claim for the next is under way meanwhile)
+            while (i >= total && cta >= 0) {
+                if (!wait(&b.claim, claims++ & 1u)) { ok = false; break; }
+                cta = i = claimed_cta(b.claimed);
+                __syncwarp();
+                if (lane == 0 && cta >= 0) {
+                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // the answer was read before the next is written
+                    claim_cta(b.claimed, &b.claim);
+                }
+            }
+            if (!ok) break;
             const uint32_t s = nitem & 1u;
             if (nitem >= 2 && !wait(&b.item_empty[s], ((nitem >> 1) - 1) & 1u)) { ok = false; break; }
-            it.valid = i < total;
+            it.valid = cta >= 0;
             if (it.valid) {
                 const int64_t pair = pairs - 1 - i / p.H;  // the last pairs of the sequences first: the longest
                 int64_t unused;
                 locate(p, pair, it, unused);
                 it.h = (int)(i % p.H);
+                i += gridDim.x;
             }
             if (lane == 0) {
                 b.items[s] = it;
@@ -249,79 +320,69 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_consta
             __syncwarp();
             ++nitem;
             if (!it.valid) break;
-            const int n0 = it.blocks(0, p.tpt), n1 = it.blocks(1, p.tpt), n = std::max(n0, n1);
-            auto load_q = [&](int x) {
-                if (qn[x] > 0 && !wait(&b.q_empty[x], (qn[x] - 1) & 1u)) return false;
-                if (lane == 0) {
-                    mbar_arrive_expect_tx(&b.q_full[x], (uint32_t)(C::kCols * p.r * p.tpt * 128));
-                    for (int c = 0; c < C::kCols; ++c)
-                        tma_load_3d(smem + x * C::kTileBytes + c * C::kBlkBytes, &qmap, &b.q_full[x], c * 64,
-                                    it.h * p.r, (int)it.row0 + it.tok0 + x * p.tpt);
-                }
-                ++qn[x];
-                return true;
-            };
+            const int n = std::max(it.blocks(0, p.tpt), it.blocks(1, p.tpt));
             auto load_kv = [&](const CUtensorMap *map, int j) {
                 if (loads >= S && !wait(&b.kv_empty[slot], phase ^ 1u)) return false;
                 uint8_t *dst = smem + C::kRing + slot * C::kTileBytes;
-                // V rows past the sequence's end within a step of 16 keys (the products leave later ones out)
-                const int in_seq = it.len - j * kKeys;
-                const bool tail = map == &vmap && in_seq < kKeys && (in_seq & 15);
-                uint64_t *bar = tail ? &b.tail : &b.kv_full[slot];
+                // a V block that ends inside a step of 16 keys goes to warp 11 first
+                uint64_t *bar = map == &vmap && it.tail(j) ? &b.landed[slot] : &b.kv_full[slot];
                 if (lane == 0) {
                     mbar_arrive_expect_tx(bar, (uint32_t)C::kTileBytes);
                     for (int c = 0; c < C::kCols; ++c)
                         tma_load_3d(dst + c * C::kBlkBytes, map, bar, c * 64, it.h, (int)it.row0 + j * kKeys);
                 }
-                if (tail) {
-                    const bool landed = wait(&b.tail, tails++ & 1u);
-                    const int chunks = (16 - (in_seq & 15)) * 8;  // of 16 bytes, per column block
-                    for (int i = lane; i < chunks * C::kCols; i += 32)
-                        *reinterpret_cast<uint4 *>(dst + i / chunks * C::kBlkBytes + in_seq * 128 + i % chunks * 16) =
-                            make_uint4(0u, 0u, 0u, 0u);
-                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&b.kv_full[slot]);
-                    if (!landed) return false;
-                }
                 ++loads;
                 if (++slot == S) { slot = 0; phase ^= 1u; }
                 return true;
             };
-            ok = load_q(0) && load_kv(&kmap, 0) && (n1 == 0 || load_q(1)) && load_kv(&vmap, 0);
-            for (int j = 1; ok && j < n; ++j) ok = load_kv(&kmap, j) && load_kv(&vmap, j);
+            for (int j = 0; ok && j < n; ++j) ok = load_kv(&kmap, j) && load_kv(&vmap, j);
             if (!ok) break;
         }
         if (lane == 0) {
-            // every issued copy must land before the CTA may exit (bounded, ignoring abort)
-            auto drain = [&](uint64_t *bar, uint32_t parity) {
-                const uint64_t t0 = global_ns();
-                while (!mbar_try_wait(bar, parity))
-                    if (global_ns() - t0 > kWaitLimitNs) { record_timeout(p.status); return; }
-            };
-            for (uint32_t j = loads > S ? loads - S : 0; j < loads; ++j) drain(&b.kv_full[j % S], (j / S) & 1u);
-            for (int x = 0; x < 2; ++x)
-                if (qn[x] > 0) drain(&b.q_full[x], (qn[x] - 1) & 1u);
-            if (tails > 0) drain(&b.tail, (tails - 1) & 1u);
+            // every issued copy (and answer) must land before the CTA may exit (bounded, ignoring abort)
+            if (cta >= 0) drain(&b.claim, claims & 1u, p.status);
+            for (uint32_t j = loads > S ? loads - S : 0; j < loads; ++j) drain(&b.kv_full[j % S], (j / S) & 1u, p.status);
         }
     } else if (wid == kMmaWarp) {
         // ------------------------------ MMAs: one thread ------------------------------
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
+        registers_dec<kOtherRegs>();
         if (elect_one()) {
             uint32_t slot = 0, phase = 0, nitem = 0;
-            uint32_t qn0 = 0, qn1 = 0, pn0 = 0, pn1 = 0;  // per tile: Q tiles and blocks so far
-            uint32_t parts0 = 0, parts1 = 0;              // bit c: the next parity of part c of P
+            struct Tile {
+                uint32_t sn, pn, qn, on;  // S and P V issued, items begun by S and by P V
+                uint32_t parts;           // bit c: the next parity of part c of P
+            };
+            struct Blocks {
+                int last0, last1, nb0, nb1, n;  // per tile: keys and blocks; blocks of the item, 0 at the end
+            };
+            Tile t0{0, 0, 0, 0, 0}, t1 = t0;
             const uint32_t base = smem_u32(smem);
             bool ok = true;
             auto next_slot = [&]() {
                 if (++slot == S) { slot = 0; phase ^= 1u; }
             };
-            // S of tile x for `keys` keys of the K block at k: S's columns hold the P of the block before, which its
-            // product must have read
-            auto scores = [&](int x, uint32_t k, int keys, uint32_t pn) {
-                if (pn > 0 && !wait(&b.pv_done[x], (pn - 1) & 1u)) return false;
+            auto ring = [&](uint32_t s) { return base + C::kRing + s * C::kTileBytes; };
+            auto next_item = [&](Blocks &it) {
+                const uint32_t is = nitem & 1u;
+                if (!wait(&b.item_full[is], (nitem >> 1) & 1u)) return false;
+                const Item i = b.items[is];
+                mbar_arrive(&b.item_empty[is]);
+                ++nitem;
+                it.last0 = i.last(0, p.tpt);
+                it.last1 = i.last(1, p.tpt);
+                it.nb0 = i.blocks(0, p.tpt);
+                it.nb1 = i.blocks(1, p.tpt);
+                it.n = i.valid ? std::max(it.nb0, it.nb1) : 0;
+                return true;
+            };
+            // S of tile x for `keys` keys, their K at k.  The softmax has taken the S before; where P lies over S, the
+            // product with V has read P as well.
+            auto scores = [&](Tile &t, int x, bool first, bool final, int keys, uint32_t k) {
+                if (first && !wait(&b.q_full[x], t.qn++ & 1u)) return false;
+                if (t.sn > 0 && !(C::kOwnP ? wait(&b.s_free[x], (t.sn - 1) & 1u) : wait(&b.pv_done[x], (t.pn - 1) & 1u)))
+                    return false;
                 tc_fence_after();
-                const uint32_t idesc = idesc_qk((keys + 15) & ~15);
+                const uint32_t idesc = idesc_qk((min(kKeys, keys) + 15) & ~15);
                 const uint32_t q = base + x * C::kTileBytes;
 #pragma unroll
                 for (int e = 0; e < D / 16; ++e) {
@@ -329,95 +390,87 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_consta
                     tc_mma_ss(tmem + 128u * x, smem_desc(q + off, 16, 1024, 2), smem_desc(k + off, 16, 1024, 2), idesc, e > 0);
                 }
                 tc_commit(&b.s_full[x]);
+                if (final) tc_commit(&b.q_empty[x]);
+                ++t.sn;
                 return true;
             };
-            // O += P V, part by part as P comes
-            auto product = [&](int x, uint32_t v, int keys, bool first, uint32_t &parts) {
+            // O += P V of tile x, part by part as P comes
+            auto product = [&](Tile &t, int x, bool first, int keys, uint32_t v) {
+                // the item before's output has been read
+                if (first && t.on++ > 0 && !wait(&b.o_free[x], t.on & 1u)) return false;
 #pragma unroll
                 for (int c = 0; c < kParts; ++c) {
                     if (c * kPart < keys) {
-                        if (!wait(&b.p_full[x][c], (parts >> c) & 1u)) return false;
-                        parts ^= 1u << c;
+                        if (!wait(&b.p_full[x][c], (t.parts >> c) & 1u)) return false;
+                        t.parts ^= 1u << c;
                         tc_fence_after();
 #pragma unroll
                         for (int e = c * (kPart / 16); e < (c + 1) * (kPart / 16); ++e)
                             if (e * 16 < keys)
-                                tc_mma_ts(tmem + 256u + (uint32_t)D * x, tmem + 128u * x + 8u * e,
+                                tc_mma_ts(tmem + 256u + (uint32_t)D * x, tmem + C::kPCol + C::kPStride * x + 8u * e,
                                           smem_desc(v + 2048u * e, C::kBlkBytes, 1024, 2), idesc_pv(D), (!first || e > 0) ? 1u : 0u);
                     }
                 }
                 tc_commit(&b.pv_done[x]);
+                ++t.pn;
                 return true;
             };
-            while (ok) {
-                const uint32_t is = nitem & 1u;
-                if (!wait(&b.item_full[is], (nitem >> 1) & 1u)) break;
-                const Item it = b.items[is];
-                mbar_arrive(&b.item_empty[is]);
-                ++nitem;
-                if (!it.valid) break;
-                const int last0 = it.last(0, p.tpt), last1 = it.last(1, p.tpt);
-                const int nb0 = it.blocks(0, p.tpt), nb1 = it.blocks(1, p.tpt), n = std::max(nb0, nb1);
-                // Q and the first K
-                uint32_t k = base + C::kRing + slot * C::kTileBytes;
-                ok = wait(&b.q_full[0], qn0++ & 1u) && wait(&b.kv_full[slot], phase) && scores(0, k, min(kKeys, last0), pn0);
-                if (!ok) break;
-                if (nb0 == 1) tc_commit(&b.q_empty[0]);
-                if (nb1 > 0) {
-                    ok = wait(&b.q_full[1], qn1++ & 1u) && scores(1, k, min(kKeys, last1), pn1);
-                    if (nb1 == 1) tc_commit(&b.q_empty[1]);
-                }
-                if (!ok) break;
+            Blocks it{}, nx{};
+            ok = next_item(it);
+            if (ok && it.n > 0) {
+                ok = wait(&b.kv_full[slot], phase) && scores(t0, 0, true, it.nb0 == 1, it.last0, ring(slot)) &&
+                     (it.nb1 == 0 || scores(t1, 1, true, it.nb1 == 1, it.last1, ring(slot)));
                 tc_commit(&b.kv_empty[slot]);
                 next_slot();
-                // Tile 0's product and next S, then tile 1's: the strict order keeps the tiles half a period apart
-                for (int j = 0; j < n; ++j) {
-                    const uint32_t vs = slot, v = base + C::kRing + vs * C::kTileBytes;
-                    const int u0 = j * kKeys, u1 = u0 + kKeys;
+            }
+            // Per block: tile 0's product and its next S (of the next item after its last block), then tile 1's; the strict
+            // order keeps the tiles half a period apart.  Where S does not wait for the product, both S come first.
+            while (ok && it.n > 0) {
+                for (int j = 0; ok && j < it.n; ++j) {
+                    const uint32_t vs = slot;
                     ok = wait(&b.kv_full[vs], phase);
-                    if (!ok) break;
                     next_slot();
-                    if (j < nb0) {
-                        ok = product(0, v, min(kKeys, last0 - u0), j == 0, parts0);
-                        ++pn0;
+                    const bool end = j + 1 == it.n;
+                    if (ok && end) ok = next_item(nx);
+                    const int jn = end ? 0 : j + 1, first = end;  // the next S: block jn
+                    const int nb0 = end ? nx.nb0 : it.nb0, nb1 = end ? nx.nb1 : it.nb1;
+                    const int left0 = (end ? nx.last0 : it.last0) - jn * kKeys, left1 = (end ? nx.last1 : it.last1) - jn * kKeys;
+                    const bool more = !end || nx.n > 0, s0 = more && jn < nb0, s1 = more && jn < nb1;
+                    const bool o0 = j < it.nb0, o1 = j < it.nb1;
+                    const uint32_t v = ring(vs), k = ring(slot);
+                    if (C::kOwnP) {
+                        ok = ok && (!more || wait(&b.kv_full[slot], phase));
+                        if (ok && s0) ok = scores(t0, 0, first, jn + 1 == nb0, left0, k);
+                        if (ok && s1) ok = scores(t1, 1, first, jn + 1 == nb1, left1, k);
+                        if (more) tc_commit(&b.kv_empty[slot]);
+                        if (ok && o0) ok = product(t0, 0, j == 0, it.last0 - j * kKeys, v);
+                        if (ok && o1) ok = product(t1, 1, j == 0, it.last1 - j * kKeys, v);
+                        tc_commit(&b.kv_empty[vs]);
+                    } else {
+                        if (ok && o0) ok = product(t0, 0, j == 0, it.last0 - j * kKeys, v);
+                        ok = ok && (!more || wait(&b.kv_full[slot], phase));
+                        if (ok && s0) ok = scores(t0, 0, first, jn + 1 == nb0, left0, k);
+                        if (ok && o1) ok = product(t1, 1, j == 0, it.last1 - j * kKeys, v);
+                        tc_commit(&b.kv_empty[vs]);
+                        if (ok && s1) ok = scores(t1, 1, first, jn + 1 == nb1, left1, k);
+                        if (more) tc_commit(&b.kv_empty[slot]);
                     }
-                    if (ok && j + 1 < n) ok = wait(&b.kv_full[slot], phase);
-                    k = base + C::kRing + slot * C::kTileBytes;
-                    if (ok && j + 1 < nb0) {
-                        ok = scores(0, k, min(kKeys, last0 - u1), pn0);
-                        if (j + 2 == nb0) tc_commit(&b.q_empty[0]);
-                    }
-                    if (ok && j < nb1) {
-                        ok = product(1, v, min(kKeys, last1 - u0), j == 0, parts1);
-                        ++pn1;
-                    }
-                    if (!ok) break;
-                    tc_commit(&b.kv_empty[vs]);
-                    if (j + 1 < nb1) {
-                        ok = scores(1, k, min(kKeys, last1 - u1), pn1);
-                        if (j + 2 == nb1) tc_commit(&b.q_empty[1]);
-                    }
-                    if (!ok) break;
-                    if (j + 1 < n) {
-                        tc_commit(&b.kv_empty[slot]);
-                        next_slot();
-                    }
+                    if (more) next_slot();
                 }
+                it = nx;
             }
             tc_commit(&b.done);
-            const uint64_t t0 = global_ns();
-            while (!mbar_try_wait(&b.done, 0))  // every MMA must complete before tensor memory is released
-                if (global_ns() - t0 > kWaitLimitNs) { record_timeout(p.status); break; }
+            drain(&b.done, 0, p.status);  // every MMA must complete before tensor memory is released
         }
         __syncwarp();
     } else if (wid < 8) {
-        // ------------------------------ softmax and output, one row per thread ------------------------------
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
+        // ------------------------------ softmax, one row per thread ------------------------------
+        registers_inc<kSoftmaxRegs>();
         const int x = wid >> 2, row = tid & 127;
         const uint32_t lane_bits = (uint32_t)((wid & 3) * 32) << 16;
-        const uint32_t s_addr = tmem + lane_bits + 128u * x, o_addr = tmem + lane_bits + 256u + (uint32_t)D * x;
-        const int row_tok = row / p.r, row_head = row - row_tok * p.r;
-        uint32_t nitem = 0, blocks_done = 0;
+        const uint32_t s_addr = tmem + lane_bits + 128u * x, p_addr = tmem + lane_bits + C::kPCol + C::kPStride * x, o_addr = tmem + lane_bits + 256u + (uint32_t)D * x;
+        const int row_tok = row / p.r;
+        uint32_t nitem = 0, blocks_done = 0, tiles_done = 0;
         bool ok = true;
         while (ok) {
             const uint32_t is = nitem & 1u;
@@ -442,7 +495,7 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_consta
                     m = top;
                     l *= keep;
                     if (j == 0) return;
-                    // the product of the block before has completed: S was issued after it
+                    // the product of the block before has completed: S was issued after it, or it was waited for
 #pragma unroll 1
                     for (int c = 0; c < D; c += 16) {
                         uint32_t w[16];
@@ -467,7 +520,7 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_consta
                         sum[e & 1] = add2_pairs(sum[e & 1], q);
                         w[e] = pack_bf16x2(q.x, q.y);
                     }
-                    tmem_st16(s_addr + 16u * c, w);
+                    tmem_st16(p_addr + 16u * c, w);
                 };
                 auto hand_over = [&](int part) {
                     tmem_wait_st();
@@ -475,11 +528,20 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_consta
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&b.p_full[x][part]);
                 };
+                // S is in registers: the next one may come; then P's columns and O, free once the product before is done
+                auto taken = [&]() {
+                    if (!C::kOwnP) return true;
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&b.s_free[x]);
+                    return blocks_done == 0 || wait(&b.pv_done[x], (blocks_done - 1) & 1u);
+                };
                 if (u0 + kKeys <= tile_tok + 1) {  // every row sees every key of the block
                     uint32_t v[kKeys / 32][32];
 #pragma unroll
                     for (int c = 0; c < kKeys / 32; ++c) tmem_ld32(s_addr + 32u * c, v[c]);
                     tmem_wait_ld();
+                    if (!taken()) { ok = false; break; }
                     float tops[4] = {m, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
                     for (int c = 0; c < kKeys / 32; ++c)
@@ -493,31 +555,31 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_consta
                         if ((c + 1) * 32 % kPart == 0) hand_over((c + 1) * 32 / kPart - 1);
                     }
                 } else {
-                    // the last blocks: 32 keys at a time, read once for the maximum and once for P (P of keys
-                    // 32 c .. covers columns of S that were read before)
-                    auto masked = [&](uint32_t v[32], int c) {
-                        tmem_ld32(s_addr + 32u * c, v);
-                        tmem_wait_ld();
-                        const int seen = min(keys, tok - u0 + 1) - 32 * c;
+                    // a last block: masked where a row does not see a key, P for the pieces of 32 keys that some row sees
+                    uint32_t v[kKeys / 32][32];
 #pragma unroll
-                        for (int e = 0; e < 32; ++e)
-                            if (e >= seen) v[e] = 0xff800000u;
-                    };
-                    float top = m;
-#pragma unroll 1
-                    for (int c = 0; c * 32 < keys; ++c) {
-                        uint32_t v[32];
-                        masked(v, c);
+                    for (int c = 0; c < kKeys / 32; ++c) tmem_ld32(s_addr + 32u * c, v[c]);
+                    tmem_wait_ld();
+                    if (!taken()) { ok = false; break; }
+                    const int seen = min(keys, tok - u0 + 1);
+                    float tops[4] = {m, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-                        for (int e = 0; e < 32; e += 2) top = max3(top, __uint_as_float(v[e]), __uint_as_float(v[e + 1]));
+                    for (int c = 0; c < kKeys / 32; ++c) {
+                        if (u0 + 32 * c + 32 > tile_tok + 1) {
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) v[c][e] = 32 * c + e >= seen ? 0xff800000u : v[c][e];
+                        }
+#pragma unroll
+                        for (int e = 0; e < 32; e += 2)
+                            tops[(e / 2) & 3] = max3(tops[(e / 2) & 3], __uint_as_float(v[c][e]), __uint_as_float(v[c][e + 1]));
                     }
-                    move_max(top);
-#pragma unroll 1
-                    for (int c = 0; c * 32 < keys; ++c) {
-                        uint32_t v[32];
-                        masked(v, c);
-                        exponentials(v, c);
-                        if ((c + 1) * 32 % kPart == 0 || (c + 1) * 32 >= keys) hand_over(c * 32 / kPart);
+                    move_max(fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3])));
+#pragma unroll
+                    for (int c = 0; c < kKeys / 32; ++c) {
+                        if (c * 32 < keys) {
+                            exponentials(v[c], c);
+                            if ((c + 1) * 32 % kPart == 0 || (c + 1) * 32 >= keys) hand_over(c * 32 / kPart);
+                        }
                     }
                 }
                 const f32x2 both = add2_pairs(sum[0], sum[1]);
@@ -526,46 +588,124 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_consta
             }
             if (!ok) break;
             if (nb == 0) continue;
-            if (!wait(&b.pv_done[x], (blocks_done - 1) & 1u)) break;
-            tc_fence_after();
-            const float inv = 1.0f / l;
-            const bool live = row < p.tpt * p.r && tok < it.len;
-            // 32 output values of a row at a time, through shared memory (16-byte pieces at piece ^ (row / 2) % 4 of
-            // the row's 64 bytes: no bank conflicts either way), so that a store instruction writes 8 rows' 64
-            // adjacent bytes and not 32 rows' 16
-            uint8_t *out = smem + C::kOutOff + wid * (32 * 64);
-            const uint64_t dst = reinterpret_cast<uint64_t>(p.o + (it.row0 + tok) * p.ldo + (it.h * p.r + row_head) * D);
-            const uint32_t alive = __ballot_sync(0xffffffffu, live);
-            const int piece = lane & 3;
-            uint64_t to[4];
+            const uint32_t buf = tiles_done++ & 1u;
+            reinterpret_cast<float *>(smem + C::kScaleOff)[(2 * x + buf) * kRows + row] = 1.0f / l;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&b.l_full[x][buf]);
+        }
+    } else if (wid >= kOutWarp) {
+        // ------------------------------ output, both tiles in turn ------------------------------
+        registers_dec<kOtherRegs>();
+        const int row = tid & 127;
+        const uint32_t lane_bits = (uint32_t)((wid & 3) * 32) << 16;
+        const int row_tok = row / p.r, row_head = row - row_tok * p.r;
+        uint8_t *out = smem + C::kOutOff + (wid & 3) * (32 * 64);
+        const int piece = lane & 3;
+        uint32_t nitem = 0, blocks[2] = {0, 0}, tiles[2] = {0, 0};
+        bool ok = true;
+        while (ok) {
+            const uint32_t is = nitem & 1u;
+            if (!wait(&b.item_full[is], (nitem >> 1) & 1u)) break;
+            const Item it = b.items[is];
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&b.item_empty[is]);
+            ++nitem;
+            if (!it.valid) break;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) to[i] = __shfl_sync(0xffffffffu, dst, 8 * i + (lane >> 2)) + 16u * piece;
+            for (int x = 0; x < 2; ++x) {
+                const int nb = it.blocks(x, p.tpt), tok = it.tok0 + x * p.tpt + row_tok;
+                if (nb == 0 || !ok) continue;
+                blocks[x] += nb;
+                const uint32_t buf = tiles[x] & 1u;
+                ok = wait(&b.l_full[x][buf], (tiles[x] >> 1) & 1u) && wait(&b.pv_done[x], (blocks[x] - 1) & 1u);
+                if (!ok) continue;
+                ++tiles[x];
+                tc_fence_after();
+                const uint32_t o_addr = tmem + lane_bits + 256u + (uint32_t)D * x;
+                const float inv = reinterpret_cast<const float *>(smem + C::kScaleOff)[(2 * x + buf) * kRows + row];
+                const bool live = row < p.tpt * p.r && tok < it.len;
+                // 32 output values of a row at a time, through shared memory (16-byte pieces at piece ^ (row / 2) % 4
+                // of the row's 64 bytes: no bank conflicts either way), so that a store instruction writes 8 rows' 64
+                // adjacent bytes and not 32 rows' 16
+                const uint64_t dst = reinterpret_cast<uint64_t>(p.o + (it.row0 + tok) * p.ldo + (it.h * p.r + row_head) * D);
+                const uint32_t alive = __ballot_sync(0xffffffffu, live);
+                uint64_t to[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) to[i] = __shfl_sync(0xffffffffu, dst, 8 * i + (lane >> 2)) + 16u * piece;
 #pragma unroll 1
-            for (int c = 0; c < D; c += 32) {
-                uint32_t w[32];
-                tmem_ld32(o_addr + (uint32_t)c, w);
-                tmem_wait_ld();
+                for (int c = 0; c < D; c += 32) {
+                    uint32_t w[32];
+                    tmem_ld32(o_addr + (uint32_t)c, w);
+                    tmem_wait_ld();
+                    if (c + 32 == D) {  // the tile's next product may write
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&b.o_free[x]);
+                    }
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    uint32_t g[4];
+                    for (int e = 0; e < 4; ++e) {
+                        uint32_t g[4];
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        g[i] = pack_bf16x2(__uint_as_float(w[8 * e + 2 * i]) * inv, __uint_as_float(w[8 * e + 2 * i + 1]) * inv);
-                    *reinterpret_cast<uint4 *>(out + lane * 64 + (e ^ ((lane >> 1) & 3)) * 16) = make_uint4(g[0], g[1], g[2], g[3]);
+                        for (int i = 0; i < 4; ++i)
+                            g[i] = pack_bf16x2(__uint_as_float(w[8 * e + 2 * i]) * inv, __uint_as_float(w[8 * e + 2 * i + 1]) * inv);
+                        *reinterpret_cast<uint4 *>(out + lane * 64 + (e ^ ((lane >> 1) & 3)) * 16) = make_uint4(g[0], g[1], g[2], g[3]);
+                    }
+                    __syncwarp();
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int r = 8 * i + (lane >> 2);
+                        const uint4 g = *reinterpret_cast<const uint4 *>(out + r * 64 + (piece ^ ((r >> 1) & 3)) * 16);
+                        if ((alive >> r) & 1u) *reinterpret_cast<uint4 *>(to[i] + 2u * c) = g;
+                    }
+                    __syncwarp();
                 }
-                __syncwarp();
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int r = 8 * i + (lane >> 2);
-                    const uint4 g = *reinterpret_cast<const uint4 *>(out + r * 64 + (piece ^ ((r >> 1) & 3)) * 16);
-                    if ((alive >> r) & 1u) *reinterpret_cast<uint4 *>(to[i] + 2u * c) = g;
-                }
-                __syncwarp();
             }
-            tc_fence_before();  // the next item's first product into O follows this warpgroup's next P
         }
     } else {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
+        // ------------------------------ Q of tile x, apart from K and V, which must not wait for a tile; V's tails ------------------------------
+        registers_dec<kOtherRegs>();
+        const int x = wid - kQueryWarp;
+        uint32_t nitem = 0, qn = 0, slot = 0, landed = 0;  // slot: the item's first K; landed: bit s the next parity of slot s
+        for (;;) {
+            const uint32_t is = nitem & 1u;
+            if (!wait(&b.item_full[is], (nitem >> 1) & 1u)) break;
+            const Item it = b.items[is];
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&b.item_empty[is]);
+            ++nitem;
+            if (!it.valid) break;
+            if (it.blocks(x, p.tpt) > 0) {
+                if (qn > 0 && !wait(&b.q_empty[x], (qn - 1) & 1u)) break;
+                if (lane == 0) {
+                    mbar_arrive_expect_tx(&b.q_full[x], (uint32_t)(C::kCols * p.r * p.tpt * 128));
+                    for (int c = 0; c < C::kCols; ++c)
+                        tma_load_3d(smem + x * C::kTileBytes + c * C::kBlkBytes, &qmap, &b.q_full[x], c * 64, it.h * p.r,
+                                    (int)it.row0 + it.tok0 + x * p.tpt);
+                }
+                __syncwarp();
+                ++qn;
+            }
+            if (x == 1) {
+                // V rows past the sequence's end within a step of 16 keys become 0 (the products leave later steps out)
+                const int n = std::max(it.blocks(0, p.tpt), it.blocks(1, p.tpt)), rows = it.tail(n - 1);
+                const uint32_t vs = (slot + 2 * n - 1) % S;
+                slot = (slot + 2 * n) % S;
+                if (rows > 0) {
+                    if (!wait(&b.landed[vs], (landed >> vs) & 1u)) break;
+                    landed ^= 1u << vs;
+                    uint8_t *v = smem + C::kRing + vs * C::kTileBytes;
+                    const int chunks = (16 - (rows & 15)) * 8;  // of 16 bytes, per column block
+                    for (int i = lane; i < chunks * C::kCols; i += 32)
+                        *reinterpret_cast<uint4 *>(v + i / chunks * C::kBlkBytes + rows * 128 + i % chunks * 16) =
+                            make_uint4(0u, 0u, 0u, 0u);
+                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&b.kv_full[vs]);
+                }
+            }
+        }
+        if (lane == 0 && qn > 0) drain(&b.q_full[x], (qn - 1) & 1u, p.status);
+        __syncwarp();
     }
 
     tc_fence_before();
@@ -574,20 +714,20 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_consta
     if (wid == kMmaWarp) tmem_dealloc(tmem, kTmemCols);
 }
 
-// SMs of the current device; the kernels' shared-memory limit is raised on its first use there.
-int sms_of_device()
+// Raises the kernels' shared-memory limit on their first use on the current device.
+bool prepare_device()
 {
-    static std::atomic<int> sms_of[128] = {};
+    static std::atomic<bool> ready[128] = {};
     int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 128) return 0;
-    int sms = sms_of[dev].load(std::memory_order_acquire);
-    if (sms == 0) {
-        if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
-        cudaFuncSetAttribute(prompt_attn_kernel<64>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<64>::kBytes + 1024);
-        cudaFuncSetAttribute(prompt_attn_kernel<128>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<128>::kBytes + 1024);
-        sms_of[dev].store(sms, std::memory_order_release);
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 128) return false;
+    if (!ready[dev].load(std::memory_order_acquire)) {
+        const cudaFuncAttribute limit = cudaFuncAttributeMaxDynamicSharedMemorySize;
+        if (cudaFuncSetAttribute(prompt_attn_kernel<64>, limit, Cfg<64>::kBytes + 1024) != cudaSuccess ||
+            cudaFuncSetAttribute(prompt_attn_kernel<128>, limit, Cfg<128>::kBytes + 1024) != cudaSuccess)
+            return false;
+        ready[dev].store(true, std::memory_order_release);
     }
-    return sms;
+    return true;
 }
 
 template <int D>
@@ -601,11 +741,10 @@ int run(const uint16_t *q, int64_t ldq, const uint16_t *k, int64_t ldk, const ui
     };
     if (!encode(&qm, q, Hq, ldq, a.r, a.tpt) || !encode(&km, k, a.H, ldk, 1, kKeys) || !encode(&vm, v, a.H, ldv, 1, kKeys))
         return -1;
-    const int sms = sms_of_device();
-    if (sms == 0) return -2;
+    if (!prepare_device()) return -2;
     // at most ceil(len / (2 tpt)) pairs of tiles per sequence
     const int64_t most = (a.M / (2 * a.tpt) + a.B) * a.H;
-    prompt_attn_kernel<D><<<(unsigned)std::min<int64_t>(most, sms), kThreads, Cfg<D>::kBytes + 1024, st>>>(qm, km, vm, a);
+    prompt_attn_kernel<D><<<(unsigned)std::min<int64_t>(most, 0x7fffffff), kThreads, Cfg<D>::kBytes + 1024, st>>>(qm, km, vm, a);
     return 0;
 }
 
