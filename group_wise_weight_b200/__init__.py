@@ -3,8 +3,9 @@ dequant-fused weight-only matmul on NVIDIA B200.
 
 Argument marshalling only.  Every step runs in the CUDA kernels of
 ``libwq.so``; this module passes device pointers, sizes and the current CUDA
-stream through ctypes and allocates output tensors with torch when the
-caller does not pass them.  There is no CPU path: the functions require CUDA
+stream through ctypes (the prompt-side calls through the compiled
+``_wq_torch.so``, which spares small calls most of their host time) and
+allocates output tensors with torch when the caller does not pass them.  There is no CPU path: the functions require CUDA
 tensors and raise if ``libwq.so`` is missing.
 
 bf16 scales and zero-points are returned as ``torch.bfloat16`` tensors (the
@@ -20,6 +21,7 @@ import torch
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libwq.so")
+BINDING_PATH = os.path.join(_PKG, "_wq_torch.so")
 HEADER_PATH = os.path.join(os.path.dirname(_PKG), "include", "wq.h")
 
 WQ_OK = 0
@@ -553,73 +555,32 @@ def wq_awq_channel_scales(magnitudes: torch.Tensor, alpha: float, col_scale=None
 
 # ---- The prompt side: per-token INT8, W8A8 INT8 matmul, norms and positions, cache stores, prompt attention ----
 
-def _on(device, fn, stream, *args):
-    """Call fn(*args, stream) with `device` current, on its current stream unless one is given."""
-    if device.index == torch.cuda.current_device():
-        _check(fn(*args, _stream_handle(stream)))
-    else:
-        with torch.cuda.device(device):
-            _check(fn(*args, _stream_handle(stream)))
+_native_module = None
 
 
-def _dense_as(t: torch.Tensor, name: str, dtype, shape, device) -> int:
-    """Address of a contiguous tensor of this type and shape on this device."""
-    ptr = _dev(t, name)
-    if t.dtype != dtype:
-        raise TypeError(f"{name} must be {dtype}")
-    if t.shape != shape:
-        raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, not on {device}")
-    _dense(t, name)
-    return ptr
+def _native():
+    """The compiled binding of these calls (raises if it has not been built)."""
+    global _native_module
+    if _native_module is None:
+        lib()
+        if not os.path.exists(BINDING_PATH):
+            raise RuntimeError(f"_wq_torch.so not found at {BINDING_PATH}: build it with "
+                               "`python -m group_wise_weight_b200.build` (or __graft_entry__.build())")
+        from . import _wq_torch
+        _wq_torch.set_raise_status(_check)
+        _native_module = _wq_torch
+    return _native_module
 
 
-def _out(t, name: str, dtype, shape, like: torch.Tensor):
-    """(tensor, address) of an output: the given one, checked, or a new one on like's device."""
-    if t is None:
-        t = like.new_empty(shape, dtype=dtype)
-        return t, t.data_ptr()
-    return t, _dense_as(t, name, dtype, shape, like.device)
-
-
-def _heads_of(t: torch.Tensor, name: str, device=None, shape=None):
-    """(address, row distance) of a bf16 [tokens][heads][D] tensor whose rows hold their heads one after another."""
-    ptr = _dev(t, name)
-    if t.dtype != torch.bfloat16 or t.dim() != 3:
-        raise TypeError(f"{name} must be a 3-D bfloat16 tensor [tokens][heads][D]")
-    if device is not None and t.device != device:
-        raise ValueError(f"{name} is on {t.device}, not on {device}")
-    if shape is not None and t.shape != shape:
-        raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
-    M, H, D = t.shape
-    ld, head, one = t.stride()
-    if (D > 1 and one != 1) or (H > 1 and head != D):
-        raise ValueError(f"{name} must hold each token's heads one after another (strides D and 1)")
-    return ptr, (ld if M > 1 else H * D)
-
-
-def _heads_out(t, name: str, shape, like: torch.Tensor):
-    """(tensor, address, row distance) of an output of heads: the given one, checked, or a new dense one."""
-    if t is None:
-        t = like.new_empty(shape)
-        return t, t.data_ptr(), shape[1] * shape[2]
-    return (t, *_heads_of(t, name, like.device, shape))
+def _handle(stream):
+    return None if stream is None else _stream_handle(stream)
 
 
 def wq_quantize_int8_tokens(x: torch.Tensor, q=None, scales=None, stream=None):
     """Symmetric INT8 with one binary32 scale per row (token) of x: [M][K] (row stride >= K) fp32 or bf16 on CUDA.
 
     Returns (q int8 [M][K], scales float32 [M]), the left operand of wq_gemm_w8a8_int8."""
-    px = _dev(x, "x")
-    if x.dim() != 2 or (x.stride(1) != 1 and x.shape[1] > 1):
-        raise ValueError("x must be a 2-D tensor with unit stride along K")
-    xtype = _wtype(x)
-    M, K = x.shape
-    q, pq = _out(q, "q", torch.int8, (M, K), x)
-    scales, ps = _out(scales, "scales", torch.float32, (M,), x)
-    _on(x.device, lib().wq_quantize_int8_tokens, stream, px, xtype, M, K, x.stride(0) if M > 1 else K, pq, ps)
-    return q, scales
+    return _native().quantize_int8_tokens(x, q, scales, _handle(stream))
 
 
 def wq_gemm_w8a8_int8_workspace_bytes(M: int, N: int, K: int) -> int:
@@ -631,25 +592,7 @@ def wq_gemm_w8a8_int8(xq: torch.Tensor, xscales: torch.Tensor, qweight: torch.Te
     """y[M][N] = (xq . qweight^T) * xscales[m] * scales[n], INT8 codes multiplied on the tensor cores with exact
     integer sums.  xq int8 [M][K] and xscales float32 [M] from wq_quantize_int8_tokens, qweight int8 [N][K] and
     scales bf16 ([N] or [N][1]) from wq_quantize_int8 with one scale per output channel.  bf16 out."""
-    pxq, dev = _dev(xq, "xq"), xq.device
-    if xq.dtype != torch.int8 or qweight.dtype != torch.int8 or xq.dim() != 2 or qweight.dim() != 2:
-        raise TypeError("xq and qweight must be 2-D int8 tensors")
-    _dense(xq, "xq")
-    M, K = xq.shape
-    N = qweight.shape[0]
-    y, py = _out(y, "y", torch.bfloat16, (M, N), xq)
-    if workspace is None:
-        with torch.cuda.device(dev):
-            need = wq_gemm_w8a8_int8_workspace_bytes(M, N, K)
-        workspace = torch.zeros(need, dtype=torch.uint8, device=dev)
-    elif workspace.device != dev:
-        raise ValueError(f"workspace is on {workspace.device}, not on {dev}")
-    _dense(workspace, "workspace")
-    _on(dev, lib().wq_gemm_w8a8_int8, stream, pxq, _dense_as(xscales, "xscales", torch.float32, (M,), dev), M, N, K,
-        _dense_as(qweight, "qweight", torch.int8, (N, K), dev),
-        _dense_as(scales, "scales", torch.bfloat16, (N,) if scales.dim() == 1 else (N, 1), dev),
-        py, _dev(workspace, "workspace"), workspace.numel() * workspace.element_size())
-    return y
+    return _native().gemm_w8a8_int8(xq, xscales, qweight, scales, y, workspace, _handle(stream))
 
 
 def wq_qk_norm_rope(q: torch.Tensor, k: torch.Tensor, positions: torch.Tensor, inv_freq: torch.Tensor, q_weight=None,
@@ -660,36 +603,8 @@ def wq_qk_norm_rope(q: torch.Tensor, k: torch.Tensor, positions: torch.Tensor, i
     positions int32 [M]; inv_freq float32 [rot / 2]: the first rot values of a head turn by position * inv_freq,
     in pairs (i, i + rot / 2), or (2i, 2i + 1) when `interleaved`.  q_out and k_out may be q and k (in place).
     Returns (q_out, k_out), dense bf16 unless given."""
-    dev = q.device
-    pq, ldq = _heads_of(q, "q")
-    M, Hq, D = q.shape
-    pk, ldk = _heads_of(k, "k", dev)
-    H = k.shape[1]
-    if k.shape[0] != M or k.shape[2] != D:
-        raise ValueError("q and k must have the same tokens and head size")
-    if inv_freq.dim() != 1:
-        raise ValueError("inv_freq must be a 1-D tensor")
-    q_out, pqo, ldqo = _heads_out(q_out, "q_out", (M, Hq, D), q)
-    k_out, pko, ldko = _heads_out(k_out, "k_out", (M, H, D), k)
-    half = inv_freq.numel()
-    _on(dev, lib().wq_qk_norm_rope, stream, pq, ldq, pk, ldk,
-        None if q_weight is None else _dense_as(q_weight, "q_weight", torch.bfloat16, (D,), dev),
-        None if k_weight is None else _dense_as(k_weight, "k_weight", torch.bfloat16, (D,), dev), float(eps),
-        _dense_as(positions, "positions", torch.int32, (M,), dev),
-        _dense_as(inv_freq, "inv_freq", torch.float32, (half,), dev), 2 * half, int(bool(interleaved)), M, Hq, H, D,
-        pqo, ldqo, pko, ldko)
-    return q_out, k_out
-
-
-def _store_rows(k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, k_codes: torch.Tensor):
-    dev = k.device
-    pk, ldk = _heads_of(k, "k")
-    pv, ldv = _heads_of(v, "v", dev, k.shape)
-    M, H, D = k.shape
-    if k_codes.dim() != 4 or k_codes.shape[2] != H:
-        raise ValueError("the codes must be [B][T][H][...] with k's heads")
-    ps = _dense_as(slots, "slots", torch.int64, (M,), dev)
-    return dev, (pk, ldk, pv, ldv, ps, M, k_codes.shape[0] * k_codes.shape[1], H, D)
+    return _native().qk_norm_rope(q, k, positions, inv_freq, q_weight, k_weight, eps, interleaved, q_out, k_out,
+                                  _handle(stream))
 
 
 def wq_kv_store_int4(k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, k_codes: torch.Tensor,
@@ -699,25 +614,14 @@ def wq_kv_store_int4(k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, k_co
     wq_decode_attention_int4 reads, in place: token m goes to sequence slots[m] // T, place slots[m] % T (int64 [M];
     a slot outside [0, B T) leaves the token out; slots of one call are distinct).  codes [B][T][H][64] uint8,
     scales and zero-points [B][T][H] bf16."""
-    dev, rows = _store_rows(k, v, slots, k_codes)
-    size = tuple(k_codes.shape[:3])
-    width = (k.shape[2] // 2,)
-    u8, bf = torch.uint8, torch.bfloat16
-    _on(dev, lib().wq_kv_store_int4, stream, *rows, _dense_as(k_codes, "k_codes", u8, size + width, dev),
-        _dense_as(k_scales, "k_scales", bf, size, dev), _dense_as(k_zeros, "k_zeros", bf, size, dev),
-        _dense_as(v_codes, "v_codes", u8, size + width, dev), _dense_as(v_scales, "v_scales", bf, size, dev),
-        _dense_as(v_zeros, "v_zeros", bf, size, dev))
+    _native().kv_store_int4(k, v, slots, k_codes, k_scales, k_zeros, v_codes, v_scales, v_zeros, _handle(stream))
 
 
 def wq_kv_store_fp8(k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, k_codes: torch.Tensor,
                     k_scale: torch.Tensor, v_codes: torch.Tensor, v_scale: torch.Tensor, stream=None) -> None:
     """The same for the fp8 (E4M3) cache of wq_decode_attention_fp8: codes [B][T][H][128] uint8, against the
     tensors' given scales (float32 [1] on the device)."""
-    dev, rows = _store_rows(k, v, slots, k_codes)
-    size = tuple(k_codes.shape[:3]) + (k.shape[2],)
-    _on(dev, lib().wq_kv_store_fp8, stream, *rows, _dense_as(k_codes, "k_codes", torch.uint8, size, dev),
-        _dense_as(k_scale, "k_scale", torch.float32, (1,), dev), _dense_as(v_codes, "v_codes", torch.uint8, size, dev),
-        _dense_as(v_scale, "v_scale", torch.float32, (1,), dev))
+    _native().kv_store_fp8(k, v, slots, k_codes, k_scale, v_codes, v_scale, _handle(stream))
 
 
 def wq_prompt_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, starts: torch.Tensor, o=None,
@@ -726,18 +630,4 @@ def wq_prompt_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, start
     adjacent, any row stride), query head j reading KV head j // (Hq // H); starts int32 [B + 1] on the device:
     sequence b owns rows starts[b] .. starts[b + 1].  Returns o bf16 [M][Hq][D]; rows of no sequence keep what they
     held (allocated here: nothing defined)."""
-    dev = q.device
-    pq, ldq = _heads_of(q, "q")
-    M, Hq, D = q.shape
-    pk, ldk = _heads_of(k, "k", dev)
-    H = k.shape[1]
-    if k.shape[0] != M or k.shape[2] != D:
-        raise ValueError("q and k must have the same tokens and head size")
-    pv, ldv = _heads_of(v, "v", dev, k.shape)
-    if starts.dim() != 1 or starts.numel() < 2:
-        raise ValueError("starts must be a 1-D tensor of at least two values")
-    B = starts.numel() - 1
-    o, po, ldo = _heads_out(o, "o", (M, Hq, D), q)
-    _on(dev, lib().wq_prompt_attention, stream, pq, ldq, pk, ldk, pv, ldv,
-        _dense_as(starts, "starts", torch.int32, (B + 1,), dev), B, M, Hq, H, D, po, ldo)
-    return o
+    return _native().prompt_attention(q, k, v, starts, o, _handle(stream))

@@ -3,8 +3,10 @@
 Each .cu under csrc/ is compiled to an object in _build/ with nvcc
 (-gencode arch=compute_100a,code=sm_100a, -O3, -lineinfo, no fast-math: the
 quantisers rely on IEEE division and round-to-nearest-even), then linked
-into group_wise_weight_b200/libwq.so.  Objects are rebuilt only when a
-source or header is newer.
+into group_wise_weight_b200/libwq.so.  The binding of the prompt-side calls
+(csrc/wq_torch.cpp, a CPython extension on torch's headers) is compiled with
+g++ into group_wise_weight_b200/_wq_torch.so and linked against libwq.so
+beside it.  Objects are rebuilt only when a source or header is newer.
 """
 from __future__ import annotations
 
@@ -13,12 +15,14 @@ import glob
 import os
 import shutil
 import subprocess
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libwq.so")
+BINDING = os.path.join(PKG, "_wq_torch.so")
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",
@@ -42,6 +46,19 @@ def _stale(target: str, inputs) -> bool:
         return True
     t = os.path.getmtime(target)
     return any(os.path.getmtime(p) > t for p in inputs)
+
+
+def _binding_command(src: str):
+    import torch
+
+    home = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
+    inc = [os.path.join(home, "include"), os.path.join(home, "include", "torch", "csrc", "api", "include"),
+           os.path.join(cuda, "include"), sysconfig.get_paths()["include"]]
+    libs = os.path.join(home, "lib")
+    return (["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}"]
+            + [f"-I{d}" for d in inc] + [src, "-o", BINDING + ".tmp", f"-L{PKG}", "-l:libwq.so", "-Wl,-rpath,$ORIGIN",
+                                         f"-L{libs}", "-ltorch_python", "-ltorch_cuda", "-ltorch_cpu", "-lc10_cuda", "-lc10"])
 
 
 def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) -> str:
@@ -71,6 +88,10 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
         cmd = [nvcc()] + ARCH + ["-shared", "-o", LIB + ".tmp"] + objs + ["-lcudart"]
         run(cmd)
         os.replace(LIB + ".tmp", LIB)
+    binding_src = os.path.join(CSRC, "wq_torch.cpp")
+    if force or _stale(BINDING, [binding_src] + glob.glob(os.path.join(ROOT, "include", "*.h"))):
+        run(_binding_command(binding_src))
+        os.replace(BINDING + ".tmp", BINDING)
     return LIB
 
 
