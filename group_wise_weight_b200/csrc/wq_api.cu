@@ -803,7 +803,7 @@ int wq_prompt_attention(const uint16_t *q, int64_t ldq, const uint16_t *k, int64
         return fail(WQ_ERR_UNSUPPORTED,
                     "%s: needs D of 64 or 128 and Hq a multiple of H with Hq / H <= 64 (D=%lld H=%lld Hq=%lld)", what,
                     (long long)D, (long long)H, (long long)Hq);
-    if (M > 0x3fffffffLL || B > 0xffffffLL || H > 65535 || Hq > 65535)
+    if (M > 0x3fffffffLL || B > 0xffffffLL || H > 65535 || Hq > 65535 || wq::prompt_attention_items(M, B, Hq, H) > 0x7fffffffLL)
         return fail(WQ_ERR_SHAPE, "%s: B, M, Hq or H too large", what);
     int rc;
     if ((rc = check_rows(what, "q", q, ldq, Hq, D)) != WQ_OK || (rc = check_rows(what, "k", k, ldk, H, D)) != WQ_OK ||
@@ -817,7 +817,7 @@ int wq_prompt_attention(const uint16_t *q, int64_t ldq, const uint16_t *k, int64
     if (!status) return fail(WQ_ERR_CUDA, "%s: no device status word", what);
     if (wq::launch_prompt_attention(q, ldq, k, ldk, v, ldv, starts, B, M, Hq, H, D, o, ldo, status,
                                     static_cast<cudaStream_t>(stream)) != 0)
-        return fail(WQ_ERR_CUDA, "%s: tensor map encoding failed", what);
+        return fail(WQ_ERR_CUDA, "%s: tensor map encoding or device set-up failed", what);
     return check_launch(what);
 }
 

@@ -186,8 +186,10 @@ void launch_kv_store(bool fp8, const uint16_t *k, int64_t ldk, const uint16_t *v
                      int64_t M, int64_t S, int64_t H, uint8_t *kc, uint16_t *ks, uint16_t *kz, const float *k8s,
                      uint8_t *vc, uint16_t *vs, uint16_t *vz, const float *v8s, cudaStream_t st);
 
-// Causal attention over packed prompts (wq_prompt_attn.cu): D in {64, 128}, Hq / H <= 64.  Returns 0, or -1 if a
-// tensor map cannot be encoded.
+// Causal attention over packed prompts (wq_prompt_attn.cu): D in {64, 128}, Hq / H <= 64.  Its grid has a CTA for
+// each of prompt_attention_items() (below 2^31, checked by the caller).  Returns 0, -1 if a tensor map cannot be
+// encoded, -2 if the device cannot be prepared.
+int64_t prompt_attention_items(int64_t M, int64_t B, int64_t Hq, int64_t H);
 int launch_prompt_attention(const uint16_t *q, int64_t ldq, const uint16_t *k, int64_t ldk, const uint16_t *v,
                             int64_t ldv, const int32_t *starts, int64_t B, int64_t M, int64_t Hq, int64_t H, int64_t D,
                             uint16_t *o, int64_t ldo, int *status, cudaStream_t st);

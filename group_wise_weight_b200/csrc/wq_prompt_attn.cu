@@ -116,42 +116,51 @@ struct Bars {
 };
 static_assert(sizeof(Bars) <= 640, "the barrier area");
 
-// Pairs of tiles of the packed batch in order; the one with index `t`: its sequence's first row and length and its
-// first token.  Whole warp; returns the number of pairs seen up to and including its sequence's, and sets `found`.
-// Bounds outside [0, M] are clamped, a sequence that ends before it begins is empty.
-__device__ __forceinline__ bool locate(const PromptArgs &p, int64_t t, Item &it, int64_t &all)
-{
-    const int lane = threadIdx.x & 31, span = 2 * p.tpt;
-    int64_t before = 0;
-    bool found = false;
-    for (int b0 = 0; b0 < p.B; b0 += 32) {
-        const int b = b0 + lane;
-        int64_t s = 0, e = 0;
-        if (b < p.B) {
-            s = std::min<int64_t>(std::max<int64_t>(p.starts[b], 0), p.M);
-            e = std::min<int64_t>(std::max<int64_t>(p.starts[b + 1], s), p.M);
+// The pairs of tiles of the packed batch: 32 sequences at a time, among those the pairs latest in their sequence (so
+// with the most keys) first, which leaves the shortest work to the end.  A warp that asks for pairs in ascending order
+// reads `starts` once.  Bounds outside [0, M] are
+// clamped, a sequence that ends before it begins is empty.
+struct Finder {
+    int next = 0;             // first sequence of the next chunk
+    int64_t before = 0;       // pairs before the chunk
+    int64_t s = 0, e = 0;     // this lane's sequence
+    int n = 0, all = 0;       // its pairs, and those of the chunk
+
+    __device__ __forceinline__ bool find(const PromptArgs &p, int64_t t, Item &it)
+    {
+        const int lane = threadIdx.x & 31, span = 2 * p.tpt;
+        if (t < before) *this = Finder();
+        for (;;) {
+            if (t < before + all) break;
+            if (next >= p.B) return false;
+            before += all;
+            const int b = next + lane;
+            next += 32;
+            s = e = 0;
+            if (b < p.B) {
+                s = std::min<int64_t>(std::max<int64_t>(p.starts[b], 0), p.M);
+                e = std::min<int64_t>(std::max<int64_t>(p.starts[b + 1], s), p.M);
+            }
+            // (no batch that fits memory comes near the bound; it keeps the sums of overlapping sequences in 32 bits)
+            n = (int)std::min<int64_t>((e - s + span - 1) / span, 1 << 25);
+            all = __reduce_add_sync(0xffffffffu, n);
         }
-        const int64_t n = (e - s + span - 1) / span;
-        int64_t upto = n;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int64_t x = __shfl_up_sync(0xffffffffu, upto, o);
-            if (lane >= o) upto += x;
+        // the largest place l in a sequence with more than u pairs at or behind it; u's rank among the sequences there
+        const int u = (int)(t - before);
+        int l = 0, none = __reduce_max_sync(0xffffffffu, n);
+        while (none - l > 1) {
+            const int mid = (l + none) / 2, pairs = __reduce_add_sync(0xffffffffu, max(0, n - mid));
+            if (pairs > u) l = mid;
+            else none = mid;
         }
-        const unsigned hit = __ballot_sync(0xffffffffu, t >= 0 && before + upto > t);
-        if (hit) {
-            const int src = __ffs(hit) - 1;
-            it.row0 = __shfl_sync(0xffffffffu, s, src);
-            it.len = (int)__shfl_sync(0xffffffffu, e - s, src);
-            it.tok0 = (int)(t - before - __shfl_sync(0xffffffffu, upto - n, src)) * span;
-            found = true;
-            break;
-        }
-        before += __shfl_sync(0xffffffffu, upto, 31);
+        const int behind = __reduce_add_sync(0xffffffffu, max(0, n - l - 1));
+        const int src = (int)__fns(__ballot_sync(0xffffffffu, n > l), 0, u - behind + 1);
+        it.row0 = __shfl_sync(0xffffffffu, s, src);
+        it.len = (int)__shfl_sync(0xffffffffu, e - s, src);
+        it.tok0 = l * span;
+        return true;
     }
-    all = before;  // the total only when nothing was found
-    return found;
-}
+};
 
 // 2^x, the hardware's approximation (denormal results flushed).
 __device__ __forceinline__ float ex2(float x)
@@ -283,43 +292,40 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_consta
         // ------------------------------ items and copies ------------------------------
         registers_dec<kOtherRegs>();
         Item it{};
-        int64_t pairs;
-        locate(p, -1, it, pairs);
-        const int64_t total = pairs * p.H;
+        Finder finder;
         uint32_t slot = 0, phase = 0, loads = 0, nitem = 0;
         bool ok = true;
         uint32_t claims = 0;
-        int64_t cta = blockIdx.x, i = cta;
+        int cta = blockIdx.x;
+        bool used = false;
         if (lane == 0) claim_cta(b.claimed, &b.claim);
         for (;;) {
-            // this CTA's items, then those of CTAs claimed from the grid (the claim for the next is under way meanwhile)
-            while (i >= total && cta >= 0) {
+            // this CTA's item, then those of CTAs claimed from the grid (the claim for the next is under way meanwhile)
+            bool found = !used && finder.find(p, cta / p.H, it);
+            used = true;
+            while (!found && cta >= 0) {
                 if (!wait(&b.claim, claims++ & 1u)) { ok = false; break; }
-                cta = i = claimed_cta(b.claimed);
+                cta = claimed_cta(b.claimed);
                 __syncwarp();
-                if (lane == 0 && cta >= 0) {
+                if (cta < 0) break;
+                if (lane == 0) {
                     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // the answer was read before the next is written
                     claim_cta(b.claimed, &b.claim);
                 }
+                found = finder.find(p, cta / p.H, it);
             }
             if (!ok) break;
             const uint32_t s = nitem & 1u;
             if (nitem >= 2 && !wait(&b.item_empty[s], ((nitem >> 1) - 1) & 1u)) { ok = false; break; }
-            it.valid = cta >= 0;
-            if (it.valid) {
-                const int64_t pair = pairs - 1 - i / p.H;  // the last pairs of the sequences first: the longest
-                int64_t unused;
-                locate(p, pair, it, unused);
-                it.h = (int)(i % p.H);
-                i += gridDim.x;
-            }
+            it.valid = found;
+            it.h = cta % p.H;
             if (lane == 0) {
                 b.items[s] = it;
                 mbar_arrive(&b.item_full[s]);
             }
             __syncwarp();
             ++nitem;
-            if (!it.valid) break;
+            if (!found) break;
             const int n = std::max(it.blocks(0, p.tpt), it.blocks(1, p.tpt));
             auto load_kv = [&](const CUtensorMap *map, int j) {
                 if (loads >= S && !wait(&b.kv_empty[slot], phase ^ 1u)) return false;
@@ -742,13 +748,18 @@ int run(const uint16_t *q, int64_t ldq, const uint16_t *k, int64_t ldk, const ui
     if (!encode(&qm, q, Hq, ldq, a.r, a.tpt) || !encode(&km, k, a.H, ldk, 1, kKeys) || !encode(&vm, v, a.H, ldv, 1, kKeys))
         return -1;
     if (!prepare_device()) return -2;
-    // at most ceil(len / (2 tpt)) pairs of tiles per sequence
-    const int64_t most = (a.M / (2 * a.tpt) + a.B) * a.H;
-    prompt_attn_kernel<D><<<(unsigned)std::min<int64_t>(most, 0x7fffffff), kThreads, Cfg<D>::kBytes + 1024, st>>>(qm, km, vm, a);
+    const unsigned grid = (unsigned)prompt_attention_items(a.M, a.B, a.r * (int64_t)a.H, a.H);
+    prompt_attn_kernel<D><<<grid, kThreads, Cfg<D>::kBytes + 1024, st>>>(qm, km, vm, a);
     return 0;
 }
 
 }  // namespace
+
+int64_t prompt_attention_items(int64_t M, int64_t B, int64_t Hq, int64_t H)
+{
+    const int64_t span = 2 * (kRows / (Hq / H));  // tokens of a pair of tiles: at most ceil(len / span) pairs per sequence
+    return (M / span + B) * H;
+}
 
 int launch_prompt_attention(const uint16_t *q, int64_t ldq, const uint16_t *k, int64_t ldk, const uint16_t *v,
                             int64_t ldv, const int32_t *starts, int64_t B, int64_t M, int64_t Hq, int64_t H, int64_t D,
