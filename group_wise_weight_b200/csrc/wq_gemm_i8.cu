@@ -41,6 +41,7 @@
 // activation rows small enough to stay in L2.
 #include <algorithm>
 #include <atomic>
+#include <type_traits>
 
 #include "wq_internal.h"
 #include "wq_sm100.cuh"
@@ -337,7 +338,7 @@ struct Stream {
     static constexpr int kStage = kOperand + BN * kRowBytes;
     static constexpr int kStages = 200 * 1024 / kStage;  // 11, 10, 8, 6
     static constexpr int kBarOff = kStages * kStage;
-    static constexpr int kSmem = kBarOff + 256;
+    static constexpr int kSmem = kBarOff + 1024;
     static constexpr uint32_t kCols = 2 * BN;  // two accumulators
 };
 
@@ -356,24 +357,35 @@ struct StreamBars {
     uint64_t full[11], empty[11], d_full[2], d_empty[2], done;
     int abort, last;
     uint32_t tmem;
+    float sx[128];
 };
-static_assert(sizeof(StreamBars) <= 256, "the barrier area");
+static_assert(sizeof(StreamBars) <= 1024, "the barrier area");
 
-// Units (tile, stage) in tile order; CTA b takes `per` of them, the first `extra` CTAs one more, the last what is left.
+// Units (tile, stage) in tile order, dealt to the CTAs in one of two ways.  split > 0: a tile's stages to `split` CTAs, `per`
+// to each (the last takes what is left), so that a CTA has one part of one tile.  split = 0: `per` to every CTA, the first
+// `extra` one more, the last what is left, wherever the tiles end.
 struct Plan {
     int64_t tiles, total;
-    int nt, stages, grid, per, extra, max_segs;
+    int nt, stages, grid, split, per, extra, max_segs;
     bool shared;  // who adds up a split tile: its CTAs, a share of the columns each, or the last of them to finish
     __host__ __device__ int64_t begin_of(int b) const
     {
-        const int64_t u = (int64_t)b * per + (b < extra ? b : extra);
-        return u < total ? u : total;
+        if (split > 0) return (int64_t)(b / split) * stages + min_of((b % split) * per, stages);
+        return min_of((int64_t)b * per + (b < extra ? b : extra), total);
+    }
+    __host__ __device__ int64_t end_of(int b) const
+    {
+        if (split > 0) return (int64_t)(b / split) * stages + min_of((b % split + 1) * per, stages);
+        return begin_of(b + 1);
     }
     __host__ __device__ int cta_of(int64_t u) const
     {
+        if (split > 0) return (int)(u / stages) * split + (int)(u % stages) / per;
         const int64_t big = (int64_t)extra * (per + 1);
         return (int)(u < big ? u / (per + 1) : extra + (u - big) / per);
     }
+    template <typename T>
+    static __host__ __device__ T min_of(T a, T b) { return a < b ? a : b; }
 };
 
 struct StreamArgs {
@@ -392,7 +404,7 @@ gemm_i8_stream_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_con
     uint8_t *smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
     StreamBars &b = *reinterpret_cast<StreamBars *>(smem + C::kBarOff);
     const int tid = threadIdx.x, wid = tid >> 5, lane = tid & 31, stages = p.plan.stages, nt = p.plan.nt;
-    const int64_t beg = p.plan.begin_of(blockIdx.x), end = p.plan.begin_of(blockIdx.x + 1);
+    const int64_t beg = p.plan.begin_of(blockIdx.x), end = p.plan.end_of(blockIdx.x);
     auto wait = [&](uint64_t *bar, uint32_t parity) { return mbar_wait(bar, parity, p.g.status, &b.abort); };
 
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -479,12 +491,20 @@ gemm_i8_stream_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_con
         const uint32_t lane_bits = (uint32_t)(quarter * 32) << 16;
         const int64_t M = p.g.M, N = p.g.N;
         uint32_t n = 0;
+        int64_t sx_at = -1;
         bool ok = true;
         for (int64_t u = beg; u < end; ++n) {
             const int64_t tile = u / stages;
             const int s0 = (int)(u - tile * stages), s1 = (int)std::min<int64_t>(stages, s0 + (end - u));
             const int64_t nr = tile % nt * 128 + r, m0 = tile / nt * BN;
             const int cols = (int)std::min<int64_t>(BN, M - m0);
+            const float sw = nr < N ? bf16_to_f32(ld_nc_u16(p.g.ws + nr)) : 0.0f;
+            if (m0 != sx_at) {  // the tokens' scales, while the MMAs run
+                named_bar_sync(1, 128);
+                if (r < cols) b.sx[r] = __ldg(p.g.xs + m0 + r);
+                named_bar_sync(1, 128);
+                sx_at = m0;
+            }
             if (!wait(&b.d_full[n & 1u], (n >> 1) & 1u)) { ok = false; break; }
             tc_fence_after();
             const uint32_t d = tmem + lane_bits + (n & 1u) * (uint32_t)BN;
@@ -493,7 +513,7 @@ gemm_i8_stream_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_con
             int *parts = p.part + tile * p.plan.max_segs * (BN * 128);
             const int first = p.plan.cta_of(tile * stages), mine = (int)blockIdx.x - first;
             const int count = whole ? 1 : p.plan.cta_of(tile * stages + stages - 1) - first + 1;
-            bool writes = whole;  // shared tiles are written below
+            bool writes = false;  // shared tiles are written below
             if (!whole) {
 #pragma unroll 1
                 for (int c = 0; c < cols; c += 16) {
@@ -516,29 +536,38 @@ gemm_i8_stream_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_con
                     if (writes) __threadfence();
                 }
             }
-            if (writes) {
-                const float sw = nr < N ? bf16_to_f32(ld_nc_u16(p.g.ws + nr)) : 0.0f;
+            // 16 columns of this row, the other parts' sums added where there are any (whole tiles have their own copy of
+            // the loop: with the parts in it they took 40% longer)
+            auto write = [&](auto parted) {
 #pragma unroll 1
                 for (int c = 0; c < cols; c += 16) {
                     uint32_t v[16];
                     tmem_ld16(d + (uint32_t)c, v);
                     tmem_wait_ld();
-                    for (int o = 0; o < count; ++o) {
-                        if (o == mine) continue;
-                        const int *from = parts + ((int64_t)o * BN + c) * 128 + r;
+                    if constexpr (decltype(parted)::value) {
+                        for (int o = 0; o < count; ++o) {
+                            if (o == mine) continue;
+                            const int *from = parts + ((int64_t)o * BN + c) * 128 + r;
 #pragma unroll
-                        for (int e = 0; e < 16; ++e)
-                            if (c + e < cols) v[e] += (uint32_t)__ldcg(from + e * 128);
+                            for (int e = 0; e < 16; ++e)
+                                if (c + e < cols) v[e] += (uint32_t)__ldcg(from + e * 128);
+                        }
                     }
                     if (nr < N) {
+                        uint16_t *to = p.g.y + (m0 + c) * N + nr;
 #pragma unroll
-                        for (int e = 0; e < 16; ++e)
-                            if (c + e < cols)
-                                p.g.y[(m0 + c + e) * N + nr] =
-                                    f32_to_bf16(__fmul_rn((float)(int)v[e], __fmul_rn(__ldg(p.g.xs + m0 + c + e), sw)));
+                        for (int e = 0; e < 16; ++e) {
+                            if (c + e < cols) *to = f32_to_bf16(__fmul_rn((float)(int)v[e], __fmul_rn(b.sx[c + e], sw)));
+                            to += N;
+                        }
                     }
                 }
-                if (!whole && tid == 64) p.counters[tile] = 0;  // every part has been counted: nobody else touches it
+            };
+            if (whole) {
+                write(std::false_type{});
+            } else if (writes) {
+                write(std::true_type{});
+                if (tid == 64) p.counters[tile] = 0;  // every part has been counted: nobody else touches it
             }
             tc_fence_before();
             __syncwarp();
@@ -647,10 +676,11 @@ int stream_bn(int64_t M) { return M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : 1
 // 26.7 (cut 31.7); M = 100, 28672 x 1024: whole 15.8 (cut 26.5); M = 100, 8192 x 28672: cut 57 (pairs 72); M = 256, 8192 x
 // 8192: pairs 27 (cut 47); M = 192, 128 x 28672: cut 17 (pairs 65).
 //   stream, whole tiles: a CTA takes ceil(tiles / SMs) tiles; nothing is added up afterwards
-//   stream, cut: every CTA takes an equal share of the units, 8 at least, and the split tiles cost kCut + M / 16
+//   stream, even: the same number of CTAs for every tile, 8 stages at least to each: kEven + BN / 32 to add the parts up
+//   stream, cut: every CTA takes an equal share of the units, 8 at least, wherever the tiles end: kCut + BN / 16
 //   pairs: ceil(tiles / pairs) tiles of 256 x 256
 // A stage takes kUnit where few CTAs run, and what HBM gives it (kUnitAll with every SM at work); a pair's kPair.
-constexpr double kUnit = 0.27, kUnitAll = 0.40, kCut = 2.0, kPair = 0.29;
+constexpr double kUnit = 0.27, kUnitAll = 0.40, kCut = 2.0, kEven = 1.0, kPair = 0.29;
 constexpr int kLeastUnits = 8;
 
 struct Choice {
@@ -667,16 +697,25 @@ Choice choose(int64_t M, int64_t N, int64_t K, int sms)
     p.tiles = (M + bn - 1) / bn * p.nt;
     p.stages = (int)((K + kRowBytes - 1) / kRowBytes);
     p.total = p.tiles * p.stages;
+    p.split = 0;
     const auto unit = [&](int64_t grid) { return std::max(kUnit, kUnitAll * (double)grid / sms); };
     const int64_t rounds = (p.tiles + sms - 1) / sms, whole_grid = (p.tiles + rounds - 1) / rounds;
     const double whole = (double)(rounds * p.stages) * unit(whole_grid);
     const int64_t cut_grid = std::max<int64_t>(1, std::min<int64_t>(sms, p.total / kLeastUnits));
     const int64_t share = (p.total + cut_grid - 1) / cut_grid;
     const double cut = (double)share * unit(cut_grid) + kCut + bn / 16;
+    const int split = (int)std::min<int64_t>(sms / std::max<int64_t>(1, p.tiles), p.stages / kLeastUnits);
+    const int part = split > 1 ? (p.stages + split - 1) / split : 0;
+    const double even = split > 1 ? part * unit(split * p.tiles) + kEven + bn / 32 : 1e30;
     const int64_t pair_tiles = ((M + kTile - 1) / kTile) * ((N + kTile - 1) / kTile);
     const double pairs = (double)((pair_tiles + sms / 2 - 1) / (sms / 2) * p.stages) * kPair;
-    c.pairs = M > 128 && pairs <= std::min(whole, cut) && pair_tiles < (1 << 30);
-    if (whole <= cut) {
+    c.pairs = M > 128 && pairs <= std::min({whole, cut, even}) && pair_tiles < (1 << 30);
+    if (even < std::min(whole, cut)) {
+        p.split = (p.stages + part - 1) / part;
+        p.grid = (int)(p.split * p.tiles);
+        p.per = part;
+        p.extra = 0;
+    } else if (whole <= cut) {
         p.grid = (int)whole_grid;
         p.per = (int)(rounds * p.stages);
         p.extra = 0;
@@ -685,7 +724,7 @@ Choice choose(int64_t M, int64_t N, int64_t K, int sms)
         p.per = (int)(p.total / p.grid);
         p.extra = (int)(p.total - (int64_t)p.per * p.grid);
     }
-    p.max_segs = whole <= cut ? 1 : (p.stages + p.per - 1) / p.per + 1;
+    p.max_segs = p.split > 0 ? p.split : p.extra == 0 && p.per % p.stages == 0 ? 1 : (p.stages + p.per - 1) / p.per + 1;
     // sharing costs a wait for the other CTAs (K = N = 8192, up to 4 parts a tile: M = 4 17.0 us without, 19.6 with), adding
     // up alone costs by parts and columns (N = 128, K = 28672, 29 parts: M = 16 26.8 us alone, 13.9 shared)
     p.shared = bn > 16 || p.max_segs * (M + 4) >= 72;
