@@ -671,16 +671,17 @@ int sms_of_device()
 
 int stream_bn(int64_t M) { return M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : 128; }
 
-// Which kernel, and how the stream's units are dealt, by the time that this model gives (microseconds).  On B200 it
-// chooses, with the other choice's time behind: M = 1, 10240 x 8192: cut 21.2 (whole 28); M = 100, 10240 x 8192: whole
-// 26.7 (cut 31.7); M = 100, 28672 x 1024: whole 15.8 (cut 26.5); M = 100, 8192 x 28672: cut 57 (pairs 72); M = 256, 8192 x
-// 8192: pairs 27 (cut 47); M = 192, 128 x 28672: cut 17 (pairs 65).
+// Which kernel, and how the stream's units are dealt, by the time that this model gives (microseconds):
 //   stream, whole tiles: a CTA takes ceil(tiles / SMs) tiles; nothing is added up afterwards
-//   stream, even: the same number of CTAs for every tile, 8 stages at least to each: kEven + BN / 32 to add the parts up
-//   stream, cut: every CTA takes an equal share of the units, 8 at least, wherever the tiles end: kCut + BN / 16
+//   stream, even: the same number of CTAs for every tile, 8 stages at least to each: BN / 16 to add the parts up
+//   stream, cut: every CTA takes an equal share of the units, 8 at least, wherever the tiles end: kCut + BN / 8
 //   pairs: ceil(tiles / pairs) tiles of 256 x 256
 // A stage takes kUnit where few CTAs run, and what HBM gives it (kUnitAll with every SM at work); a pair's kPair.
-constexpr double kUnit = 0.27, kUnitAll = 0.40, kCut = 2.0, kEven = 1.0, kPair = 0.29;
+// What it chooses on B200, measured, with the others' times behind: M = 1, N = 10240, K = 8192: whole 18.8 (cut 20.3);
+// M = 64, 8192 x 8192: even 19.4 (whole 20.8, cut 25); M = 100, 8192 x 28672: even 52 (cut 59); M = 128, 2048 x 8192: even 14
+// (whole 22); M = 256, 8192 x 8192: whole 24.0 (pairs 26.8); M = 256, 10240 x 8192: pairs 28 (stream 40); M = 192, 130 x
+// 28672: even 18 (pairs 70).
+constexpr double kUnit = 0.23, kUnitAll = 0.36, kCut = 2.0, kPair = 0.33;
 constexpr int kLeastUnits = 8;
 
 struct Choice {
@@ -703,10 +704,10 @@ Choice choose(int64_t M, int64_t N, int64_t K, int sms)
     const double whole = (double)(rounds * p.stages) * unit(whole_grid);
     const int64_t cut_grid = std::max<int64_t>(1, std::min<int64_t>(sms, p.total / kLeastUnits));
     const int64_t share = (p.total + cut_grid - 1) / cut_grid;
-    const double cut = (double)share * unit(cut_grid) + kCut + bn / 16;
+    const double cut = (double)share * unit(cut_grid) + kCut + bn / 8;
     const int split = (int)std::min<int64_t>(sms / std::max<int64_t>(1, p.tiles), p.stages / kLeastUnits);
     const int part = split > 1 ? (p.stages + split - 1) / split : 0;
-    const double even = split > 1 ? part * unit(split * p.tiles) + kEven + bn / 32 : 1e30;
+    const double even = split > 1 ? part * unit(split * p.tiles) + bn / 16 : 1e30;
     const int64_t pair_tiles = ((M + kTile - 1) / kTile) * ((N + kTile - 1) / kTile);
     const double pairs = (double)((pair_tiles + sms / 2 - 1) / (sms / 2) * p.stages) * kPair;
     c.pairs = M > 128 && pairs <= std::min({whole, cut, even}) && pair_tiles < (1 << 30);
