@@ -35,7 +35,6 @@ constexpr int kD = 128;
 constexpr int kLanes = kD / 16;  // lanes per vector
 constexpr int kThreads = 256;
 constexpr int kGroups = kThreads / kLanes;
-constexpr int kUnroll = 2;       // vectors in flight per group of 8 lanes
 
 struct StoreArgs {
     const uint16_t *k, *v;
@@ -153,51 +152,38 @@ __device__ __forceinline__ uint4 fp8_codes(const uint4 raw[2], float s)
     return make_uint4(word[0], word[1], word[2], word[3]);
 }
 
-// Vector index j runs over (token, K or V, head): a token's heads are adjacent, so are their groups of lanes.
+// Vector index j runs over (token, K or V, head): a token's heads are adjacent, so are their groups of lanes.  One
+// vector per group and CTA (two in flight per lane measured 10% slower at 16,000 tokens of 8 heads, four 25%).
 template <bool FP8>
 __global__ void __launch_bounds__(kThreads)
 kv_store_kernel(const StoreArgs p)
 {
-    const unsigned l = threadIdx.x % kLanes, g = threadIdx.x / kLanes, H = (unsigned)p.H;
-    const unsigned vectors = (unsigned)p.M * 2u * H;
-    const unsigned j0 = blockIdx.x * (kGroups * kUnroll) + g;
-    uint4 raw[kUnroll][2];
-    int64_t slot[kUnroll], row[kUnroll];
-    bool is_v[kUnroll];
-#pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
-        const unsigned j = j0 + u * kGroups;
-        slot[u] = -1;
-        raw[u][0] = raw[u][1] = make_uint4(0u, 0u, 0u, 0u);
-        row[u] = 0;
-        is_v[u] = false;
-        if (j < vectors) {
-            const unsigned m = j / (2u * H), rest = j - m * 2u * H;
-            is_v[u] = rest >= H;
-            const unsigned h = is_v[u] ? rest - H : rest;
-            slot[u] = __ldg(p.slots + m);
-            if (slot[u] >= p.S) slot[u] = -1;
-            const uint16_t *src = (is_v[u] ? p.v + m * p.ldv : p.k + m * p.ldk) + h * kD + l * 16;
-            raw[u][0] = ld_stream_v4(src);
-            raw[u][1] = ld_stream_v4(src + 8);
-            row[u] = slot[u] * H + h;
-        }
+    const unsigned l = threadIdx.x % kLanes, H = (unsigned)p.H, j = blockIdx.x * kGroups + threadIdx.x / kLanes;
+    int64_t slot = -1, row = 0;
+    uint4 raw[2] = {make_uint4(0u, 0u, 0u, 0u), make_uint4(0u, 0u, 0u, 0u)};
+    bool is_v = false;
+    if (j < (unsigned)p.M * 2u * H) {
+        const unsigned m = j / (2u * H), rest = j - m * 2u * H;
+        is_v = rest >= H;
+        const unsigned h = is_v ? rest - H : rest;
+        slot = __ldg(p.slots + m);
+        if (slot >= p.S) slot = -1;
+        const uint16_t *src = (is_v ? p.v + m * p.ldv : p.k + m * p.ldk) + h * kD + l * 16;
+        raw[0] = ld_stream_v4(src);
+        raw[1] = ld_stream_v4(src + 8);
+        row = slot * H + h;
     }
-    const float ks = FP8 ? __ldg(p.k8s) : 0.0f, vs = FP8 ? __ldg(p.v8s) : 0.0f;
-#pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
-        if (FP8) {
-            const uint4 c = fp8_codes(raw[u], is_v[u] ? vs : ks);
-            if (slot[u] >= 0) *reinterpret_cast<uint4 *>((is_v[u] ? p.vc : p.kc) + row[u] * kD + l * 16) = c;
-        } else {
-            float s, z;
-            const uint2 c = int4_block(raw[u], s, z);
-            if (slot[u] >= 0) {
-                *reinterpret_cast<uint2 *>((is_v[u] ? p.vc : p.kc) + row[u] * (kD / 2) + l * 8) = c;
-                if (l == 0) {
-                    (is_v[u] ? p.vs : p.ks)[row[u]] = f32_to_bf16(s);
-                    (is_v[u] ? p.vz : p.kz)[row[u]] = f32_to_bf16(z);
-                }
+    if (FP8) {
+        const uint4 c = fp8_codes(raw, __ldg(is_v ? p.v8s : p.k8s));
+        if (slot >= 0) *reinterpret_cast<uint4 *>((is_v ? p.vc : p.kc) + row * kD + l * 16) = c;
+    } else {
+        float s, z;
+        const uint2 c = int4_block(raw, s, z);
+        if (slot >= 0) {
+            *reinterpret_cast<uint2 *>((is_v ? p.vc : p.kc) + row * (kD / 2) + l * 8) = c;
+            if (l == 0) {
+                (is_v ? p.vs : p.ks)[row] = f32_to_bf16(s);
+                (is_v ? p.vz : p.kz)[row] = f32_to_bf16(z);
             }
         }
     }
@@ -210,8 +196,7 @@ void launch_kv_store(bool fp8, const uint16_t *k, int64_t ldk, const uint16_t *v
                      uint8_t *vc, uint16_t *vs, uint16_t *vz, const float *v8s, cudaStream_t st)
 {
     const StoreArgs a{k, v, ldk, ldv, slots, M, S, (int)H, kc, vc, ks, kz, vs, vz, k8s, v8s};
-    const int64_t per = (int64_t)kGroups * kUnroll;
-    const unsigned grid = (unsigned)((M * 2 * H + per - 1) / per);
+    const unsigned grid = (unsigned)((M * 2 * H + kGroups - 1) / kGroups);
     if (fp8) kv_store_kernel<true><<<grid, kThreads, 0, st>>>(a);
     else kv_store_kernel<false><<<grid, kThreads, 0, st>>>(a);
 }

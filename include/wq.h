@@ -511,9 +511,17 @@ size_t wq_gemm_w8a8_int8_workspace_bytes(int64_t M, int64_t N, int64_t K);
  * after it is binary32, round to nearest even: y is defined bit by bit.
  * Requirements: M, N >= 1; K >= 32, K % 32 == 0, K < 131072; xq, qweight,
  * scales, y 16-byte aligned, xscales 4-byte; workspace of
- * wq_gemm_w8a8_int8_workspace_bytes bytes, not overlapping y; y must not
- * overlap an input.  Split tiles are combined by the CTA of their first
- * segment, as described under wq_gemm_w4a16.
+ * wq_gemm_w8a8_int8_workspace_bytes bytes (may be NULL when that is 0), not
+ * overlapping y; y must not overlap an input.
+ * Kernels, chosen by a model of their times: one that streams the weights
+ * (128 of their rows by up to 128 tokens per tile, a tile's K cut between CTAs
+ * where that pays), and for many tokens one that computes 256 x 256 tiles on
+ * pairs of SMs and needs no workspace.  The streaming kernel is launched with
+ * programmatic dependent launch, reads and writes nothing before the previous
+ * kernel on the stream has completed, and runs at most one CTA per SM; the
+ * CTAs of a cut tile may wait for one another's sums, and a kernel on another
+ * stream that holds SMs for good would make that wait run out
+ * (WQ_ERR_DEVICE_TIMEOUT from wq_device_status after 1 s) rather than hang.
  */
 int wq_gemm_w8a8_int8(const int8_t *xq, const float *xscales, int64_t M, int64_t N, int64_t K, const int8_t *qweight,
                       const uint16_t *scales, uint16_t *y, void *workspace, size_t ws_bytes, void *stream);
@@ -590,8 +598,10 @@ int wq_kv_store_fp8(const uint16_t *k, int64_t ldk, const uint16_t *v, int64_t l
  * give identical bytes.
  * Requirements: B, M >= 1; D 64 or 128, Hq % H == 0, Hq / H <= 64
  * (WQ_ERR_UNSUPPORTED otherwise); row distances >= heads * D and multiples of
- * 8; q, k, v, o 16-byte aligned, starts 4-byte; o must not overlap an input
- * (columns of one buffer, with the same row distance, are apart).
+ * 8; q, k, v, o 16-byte aligned, starts 4-byte; (M * Hq / 256 + B) * H below
+ * 2^31; o must not overlap an input (columns of one buffer, with the same row
+ * distance, are apart).  `starts` that break the rule above are clamped: what
+ * they ask for is unspecified, but nothing outside the M rows is touched.
  */
 int wq_prompt_attention(const uint16_t *q, int64_t ldq, const uint16_t *k, int64_t ldk, const uint16_t *v, int64_t ldv,
                         const int32_t *starts, int64_t B, int64_t M, int64_t Hq, int64_t H, int64_t D, uint16_t *o,
