@@ -19,8 +19,9 @@
 // sums in the workspace and adds its stages to the tile's counter.  With few
 // parts and tokens the one that completes the counter adds the parts up
 // (exact, so in any order) and writes y; with more, every CTA of the tile
-// comes back at the end of its units, waits for the counter (bounded: the
-// parts of others never wait for this) and does a share of the columns.  The
+// comes back at the end of its units, waits for the counter (bounded, and the
+// launch is cooperative: the parts of others never wait for this) and does a
+// share of the columns.  The
 // ring takes 200 KB: what an SM has in flight sets the rate (M = 1, N = 57344,
 // K = 8192: 6 stages of 18 KB 81.6 us, 11 stages 72.8 us, 6.45 TB/s).  The kernel
 // is launched to set up while the previous one ends (0.4 us of a call; asking
@@ -38,7 +39,9 @@
 // pair's MMAs and their commits, which reach both CTAs; warps 2-5 turn one of
 // two accumulators into bf16 while the MMAs fill the other.  Tiles are taken
 // round-robin in an order that walks the weight columns within a band of
-// activation rows small enough to stay in L2.
+// activation rows small enough to stay in L2.  Measured: M = 8,190, N = 57,344,
+// K = 8,192 in 2.27 ms, 3,390 TOPS with the tensor pipe 89% busy (2.69 ms
+// once the power cap lowers the clock); 2,048 x 8,192 x 8,192 94 us.
 #include <algorithm>
 #include <atomic>
 #include <type_traits>
@@ -752,11 +755,15 @@ int run_stream(const int8_t *xq, const int8_t *wq, const Args &g, const Plan &pl
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = C::kSmem + 1024;
     cfg.stream = st;
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
+    // CTAs that wait for one another start together or not at all, whatever else holds SMs (no time lost: M = 100, 8192 x
+    // 28672 52.4 us, 52.7 without)
+    attr[1].id = cudaLaunchAttributeCooperative;
+    attr[1].val.cooperative = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = plan.max_segs > 1 && plan.shared ? 2 : 1;
     cudaLaunchKernelEx(&cfg, gemm_i8_stream_kernel<BN>, xmap, wmap, a);  // a failure is the caller's last error
     return 0;
 }

@@ -22,6 +22,10 @@
 // (wq_quotient.cuh): one correction step for the bf16 scales of int4, two for
 // the arbitrary binary32 scale of fp8; blocks outside the proven range use
 // the IEEE division.
+// Measured, 16,000 tokens of 8 heads: fp8 20.7 us (4.7 TB/s), int4 25 us (3.3
+// TB/s); the schedulers issue 70% of the time, so the instructions bind.  The
+// blocks of a lane are left to other warps (one vector per group of lanes):
+// several in turn per warp took 22.8 us.
 #include <algorithm>
 
 #include "wq_internal.h"

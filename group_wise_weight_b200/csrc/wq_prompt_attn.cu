@@ -33,11 +33,21 @@
 // tiles are half a period apart: while one's warpgroup is in its softmax the
 // tensor core works on the other.  The block's two products take 1,024 cycles
 // of the tensor core per tile and its 16,384 exponentials as many of the
-// special-function units, so both are at their limits together.
+// special-function units, so both are at their limits together (heads of 64:
+// half the products, the exponentials alone).  Measured, causal halves only:
+// one sequence of 16,384 tokens, 64 query and 8 KV heads of 128, 3.34 ms
+// (1,317 TFLOP/s; 3.94 ms once the power cap lowers the clock); 32 query heads
+// of 64, 1.35 ms (817).  Short prompts lose the ends: 48 of 1 to 331 tokens,
+// 64 query heads, 82 us.  A block of 64 keys with two S tiles, a polynomial for
+// part of the exponentials, softmax warpgroups that take turns and key blocks
+// asked into L2 ahead each gained nothing.
 //
 // Roles (512 threads): warps 0-3 and 4-7 the two softmax warpgroups, warp 8 the
 // items and a ring of K and V blocks, one thread of warp 9 the MMAs, warps 10
-// and 11 a tile's Q each (the next item's as soon as the tile is free), warps 12-15 the outputs: O / l in bf16 while the tile's warpgroup is at the next item.
+// and 11 a tile's Q each (the next item's as soon as the tile is free), warps
+// 12-15 the outputs: O / l in bf16 while the tile's warpgroup is at the next
+// item.  Registers: 512 threads of 128 at launch, split 184 to a softmax thread
+// and 72 to another.
 // Keys past a tile's last visible one are left out of both products in steps
 // of 16; inside the step their p is 0, and the copy warp zeroes the V rows past
 // the sequence's end, so what lies behind a sequence never enters a sum.
@@ -285,8 +295,6 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_consta
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = b.tmem;
-
-    // 384 threads of 168 registers at launch: 200 for the softmax warpgroups, 104 for the third
 
     if (wid == kLoadWarp) {
         // ------------------------------ items and copies ------------------------------

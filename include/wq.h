@@ -518,10 +518,10 @@ size_t wq_gemm_w8a8_int8_workspace_bytes(int64_t M, int64_t N, int64_t K);
  * where that pays), and for many tokens one that computes 256 x 256 tiles on
  * pairs of SMs and needs no workspace.  The streaming kernel is launched with
  * programmatic dependent launch, reads and writes nothing before the previous
- * kernel on the stream has completed, and runs at most one CTA per SM; the
- * CTAs of a cut tile may wait for one another's sums, and a kernel on another
- * stream that holds SMs for good would make that wait run out
- * (WQ_ERR_DEVICE_TIMEOUT from wq_device_status after 1 s) rather than hang.
+ * kernel on the stream has completed, and runs at most one CTA per SM; where
+ * the CTAs of a cut tile wait for one another's sums the launch is a
+ * cooperative one, so that calls on several streams never hold the SMs that
+ * the other waits for (every wait is bounded all the same).
  */
 int wq_gemm_w8a8_int8(const int8_t *xq, const float *xscales, int64_t M, int64_t N, int64_t K, const int8_t *qweight,
                       const uint16_t *scales, uint16_t *y, void *workspace, size_t ws_bytes, void *stream);
@@ -592,10 +592,13 @@ int wq_kv_store_fp8(const uint16_t *k, int64_t ldk, const uint16_t *v, int64_t l
  *             sequences may be empty
  *   o         rows of Hq heads of D bf16 values, ldo apart; rows of no sequence
  *             (before starts[0], from starts[B] on) are left as they were, and
- *             what q, k and v hold there (infinities and NaN too) changes nothing
+ *             what q, k and v hold there, or in another sequence's rows
+ *             (infinities and NaN too), changes nothing
  * Scores, the running maximum and sum and the accumulator are binary32; p
  * is rounded to bf16 as the second product's operand, o once.  Repeated calls
- * give identical bytes.
+ * give identical bytes.  Within a sequence, an infinity or NaN in k or v at
+ * token u leaves o unspecified from 127 tokens before u on (a product over 16
+ * keys multiplies v by the zeros of unseen keys), in q at its own token.
  * Requirements: B, M >= 1; D 64 or 128, Hq % H == 0, Hq / H <= 64
  * (WQ_ERR_UNSUPPORTED otherwise); row distances >= heads * D and multiples of
  * 8; q, k, v, o 16-byte aligned, starts 4-byte; (M * Hq / 256 + B) * H below

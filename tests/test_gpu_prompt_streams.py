@@ -116,3 +116,32 @@ def test_matmul_right_behind_the_weight_quantiser():
         wq.wq_quantize_int8(w[i % 2], qweight=q, scales=sc)
         y = wq.wq_gemm_w8a8_int8(a, s, q, sc, workspace=space)
         assert torch.equal(y, want[i % 2])
+
+
+def test_matmuls_whose_parts_wait_on_streams_of_two_priorities():
+    """Shapes that fill every SM with CTAs that add up a tile together, on streams that compete for the SMs, with calls of
+    other sizes between: nobody may wait for a CTA that cannot start."""
+    g = torch.Generator(device="cuda").manual_seed(7)
+    codes = lambda *s: torch.randint(-127, 128, s, generator=g, device="cuda", dtype=torch.int8)  # noqa: E731
+    jobs = []
+    for M, N, K in ((100, 8192, 4096), (64, 9472, 2048), (32, 1280, 8192), (1, 1000, 28672)):
+        a, w = codes(M, K), codes(N, K)
+        sx, sw = torch.rand(M, generator=g, device="cuda"), torch.rand(N, generator=g, device="cuda").to(torch.bfloat16)
+        jobs.append((a, sx, w, sw, wq.wq_gemm_w8a8_int8(a, sx, w, sw)))
+    fill = torch.randn(1 << 22, device="cuda")
+    streams = [torch.cuda.Stream(priority=p) for p in (0, -1, 0)]
+    space = [torch.zeros(max(wq.wq_gemm_w8a8_int8_workspace_bytes(a.shape[0], w.shape[0], a.shape[1]) for a, _, w, _, _ in jobs),
+                         dtype=torch.uint8, device="cuda") for _ in streams]
+    torch.cuda.synchronize()
+    got = [[] for _ in streams]
+    for i in range(60):
+        for s, stream in enumerate(streams):
+            with torch.cuda.stream(stream):
+                if (i + s) % 5 == 0:
+                    fill.mul(1.5)
+                a, sx, w, sw, _ = jobs[(i + s) % len(jobs)]
+                got[s].append(wq.wq_gemm_w8a8_int8(a, sx, w, sw, workspace=space[s]))
+    torch.cuda.synchronize()
+    for s in range(len(streams)):
+        for i, y in enumerate(got[s]):
+            assert torch.equal(y, jobs[(i + s) % len(jobs)][4])
