@@ -43,7 +43,7 @@ def test_quantize_int8_tokens_rejects(L, kw, code):
     (dict(ws=None), WORKSPACE), (dict(wsb=1024), WORKSPACE), (dict(ws=R + 8), WORKSPACE), (dict(ws=Y), ARG),
 ])
 def test_gemm_w8a8_int8_rejects(L, kw, code):
-    a = dict(x=X, xs=S, M=1, N=10240, K=8192, w=W, s=Z, y=Y, ws=R, wsb=1 << 27)
+    a = dict(x=X, xs=S, M=1, N=1000, K=28672, w=W, s=Z, y=Y, ws=R, wsb=1 << 27)
     a.update(kw)
     assert L.wq_gemm_w8a8_int8(a["x"], a["xs"], a["M"], a["N"], a["K"], a["w"], a["s"], a["y"], a["ws"], a["wsb"],
                                None) == code
@@ -52,7 +52,7 @@ def test_gemm_w8a8_int8_rejects(L, kw, code):
 
 def test_gemm_w8a8_int8_workspace_holds_the_counters(L):
     assert wq.wq_gemm_w8a8_int8_workspace_bytes(0, 16, 64) == 0
-    assert wq.wq_gemm_w8a8_int8_workspace_bytes(1, 10240, 8192) > 65536  # tiles split between CTAs
+    assert wq.wq_gemm_w8a8_int8_workspace_bytes(1, 1000, 28672) > 65536  # tiles split between CTAs
     assert wq.wq_gemm_w8a8_int8_workspace_bytes(4096, 10240, 8192) == 0  # none split
     for M in (1, 5, 16, 17, 64, 100, 128, 129, 1000):
         for N, K in ((1, 32), (130, 28672), (512, 512), (8192, 8192), (57344, 1024), (10240, 131040)):
