@@ -803,7 +803,7 @@ int wq_prompt_attention(const uint16_t *q, int64_t ldq, const uint16_t *k, int64
         return fail(WQ_ERR_UNSUPPORTED,
                     "%s: needs D of 64 or 128 and Hq a multiple of H with Hq / H <= 64 (D=%lld H=%lld Hq=%lld)", what,
                     (long long)D, (long long)H, (long long)Hq);
-    if (M > 0x3fffffffLL || B > 0xffffffLL || H > 65535 || Hq > 65535 || wq::prompt_attention_items(M, B, Hq, H) > 0x7fffffffLL)
+    if (M > (1LL << 25) || B > (1LL << 20) || H > 65535 || Hq > 65535 || wq::prompt_attention_items(M, B, Hq, H) > 0x7fffffffLL)
         return fail(WQ_ERR_SHAPE, "%s: B, M, Hq or H too large", what);
     int rc;
     if ((rc = check_rows(what, "q", q, ldq, Hq, D)) != WQ_OK || (rc = check_rows(what, "k", k, ldk, H, D)) != WQ_OK ||

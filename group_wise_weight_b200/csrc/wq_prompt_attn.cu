@@ -68,6 +68,7 @@ constexpr int kThreads = 512;
 constexpr int kLoadWarp = 8, kMmaWarp = 9, kQueryWarp = 10, kOutWarp = 12;
 constexpr int kSoftmaxRegs = 184, kOtherRegs = 72;  // 256 threads each, of 128 at launch
 constexpr int kPart = 64, kParts = kKeys / kPart;  // keys of P that are handed to the tensor core at a time
+constexpr int kMisses = 4096;  // claims in a row that brought no item
 constexpr uint32_t kTmemCols = 512;
 constexpr float kSlack = 8.0f;  // log2 of the growth of p that is let pass before m moves
 
@@ -304,19 +305,23 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_consta
         uint32_t slot = 0, phase = 0, loads = 0, nitem = 0;
         bool ok = true;
         uint32_t claims = 0;
-        int cta = blockIdx.x;
-        bool used = false;
+        int cta = blockIdx.x, misses = 0;
+        bool claiming = true;  // an answer is under way or unread
         if (lane == 0) claim_cta(b.claimed, &b.claim);
+        bool found = finder.find(p, cta / p.H, it);
         for (;;) {
             // this CTA's item, then those of CTAs claimed from the grid (the claim for the next is under way meanwhile)
-            bool found = !used && finder.find(p, cta / p.H, it);
-            used = true;
-            while (!found && cta >= 0) {
-                if (!wait(&b.claim, claims++ & 1u)) { ok = false; break; }
-                cta = claimed_cta(b.claimed);
+            while (!found && claiming) {
+                if (!wait(&b.claim, claims & 1u)) { ok = false; break; }
+                ++claims;
+                const int next = claimed_cta(b.claimed);
                 __syncwarp();
-                if (cta < 0) break;
-                if (lane == 0) {
+                // The grid has up to a pair per sequence too many: a long run of those ends the CTA before the waits of
+                // its other warps run out.
+                claiming = next >= 0 && ++misses < kMisses;
+                if (next < 0) break;
+                cta = next;
+                if (lane == 0 && claiming) {
                     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // the answer was read before the next is written
                     claim_cta(b.claimed, &b.claim);
                 }
@@ -326,6 +331,7 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_consta
             const uint32_t s = nitem & 1u;
             if (nitem >= 2 && !wait(&b.item_empty[s], ((nitem >> 1) - 1) & 1u)) { ok = false; break; }
             it.valid = found;
+            misses = 0;
             it.h = cta % p.H;
             if (lane == 0) {
                 b.items[s] = it;
@@ -334,6 +340,7 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_consta
             __syncwarp();
             ++nitem;
             if (!found) break;
+            found = false;
             const int n = std::max(it.blocks(0, p.tpt), it.blocks(1, p.tpt));
             auto load_kv = [&](const CUtensorMap *map, int j) {
                 if (loads >= S && !wait(&b.kv_empty[slot], phase ^ 1u)) return false;
@@ -354,7 +361,7 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_consta
         }
         if (lane == 0) {
             // every issued copy (and answer) must land before the CTA may exit (bounded, ignoring abort)
-            if (cta >= 0) drain(&b.claim, claims & 1u, p.status);
+            if (claiming) drain(&b.claim, claims & 1u, p.status);
             for (uint32_t j = loads > S ? loads - S : 0; j < loads; ++j) drain(&b.kv_full[j % S], (j / S) & 1u, p.status);
         }
     } else if (wid == kMmaWarp) {

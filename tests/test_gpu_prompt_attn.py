@@ -99,6 +99,15 @@ def test_many_sequences():
     run(lengths, 8, 2, 128, 4)
 
 
+def test_long_runs_of_empty_sequences():
+    """Far more CTAs than items: few short sequences among thousands of empty ones, at the end of the batch."""
+    for B, heads in ((3000, 4), (16384, 64)):
+        starts = [0] * (B - 4) + [5, 5, 40, 41, 300]
+        q, k, v = qkv(300, heads, heads, 64, 9)
+        o = wq.wq_prompt_attention(q, k, v, torch.tensor(starts, dtype=torch.int32).cuda())
+        check(o, q, k, v, [0, 5, 40, 41, 300])
+
+
 def test_long_sequences():
     run([4100, 3000], 8, 1, 128, 5)
     run([5003], 2, 2, 64, 6)

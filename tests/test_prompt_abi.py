@@ -126,7 +126,9 @@ def _attn(L, **kw):
     (dict(q=None), ARG), (dict(k=None), ARG), (dict(v=None), ARG), (dict(st=None), ARG), (dict(o=None), ARG),
     (dict(B=0), ARG), (dict(M=0), ARG), (dict(H=0), ARG), (dict(D=80), UNSUPPORTED), (dict(D=256), UNSUPPORTED),
     (dict(H=3, ldk=384, ldv=384), UNSUPPORTED), (dict(Hq=130, H=2, ldq=130 * 128, ldo=130 * 128), UNSUPPORTED),
-    (dict(M=1 << 31), SHAPE), (dict(ldq=1000), SHAPE), (dict(ldo=1016), SHAPE), (dict(ldv=100), SHAPE),
+    (dict(M=1 << 31), SHAPE), (dict(M=(1 << 25) + 1), SHAPE), (dict(B=(1 << 20) + 1), SHAPE),
+    (dict(B=1 << 20, Hq=60000, H=60000, ldq=60000 * 128, ldk=60000 * 128, ldv=60000 * 128, ldo=60000 * 128), SHAPE),
+    (dict(ldq=1000), SHAPE), (dict(ldo=1016), SHAPE), (dict(ldv=100), SHAPE),
     (dict(ldk=260), ALIGN), (dict(q=X + 8), ALIGN), (dict(o=Y + 4), ALIGN), (dict(st=S + 2), ALIGN),
     (dict(o=X), ARG), (dict(o=Q + 16), ARG), (dict(o=W + 256 * 99 * 2), ARG), (dict(o=S), ARG),
 ])
