@@ -71,9 +71,7 @@ __device__ __forceinline__ float round_bf16(float f) { return bf16_to_f32(f32_to
 // Pack two binary32 into a bf16x2 word (lo = a, hi = b), each rounded to nearest even.
 __device__ __forceinline__ uint32_t pack_bf16x2(float a, float b)
 {
-    uint32_t r;
-    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
-    return r;
+    return (uint32_t)f32_to_bf16(a) | ((uint32_t)f32_to_bf16(b) << 16);
 }
 
 // (128 + q) - (128 + z) on a bf16 pair: exact for the integers of a code and a zero-point (any integer of

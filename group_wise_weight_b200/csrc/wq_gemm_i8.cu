@@ -47,7 +47,7 @@
 #include <type_traits>
 
 #include "wq_internal.h"
-#include "wq_sm100.cuh"
+#include "wq_prompt.cuh"
 
 namespace wq {
 
@@ -139,14 +139,6 @@ __host__ __device__ constexpr uint32_t idesc_s8_s32(int m, int n)
     return (2u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(m >> 4) << 24);
 }
 
-// One lane of the (whole) warp.
-__device__ __forceinline__ bool elect_one()
-{
-    uint32_t p;
-    asm volatile("{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\tselp.u32 %0, 1, 0, q;\n\t}" : "=r"(p));
-    return p != 0;
-}
-
 // Tile t in order: bands of row tiles; within one, column by column.
 __device__ __forceinline__ void tile_at(const Args &p, int t, int &mi, int &ni)
 {
@@ -190,6 +182,8 @@ gemm_i8_pair_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_const
     cluster_sync();
     tc_fence_after();
     const uint32_t tmem = b.tmem;
+    asm volatile("griddepcontrol.wait;" ::: "memory");  // what came before on the stream is complete from here on
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
     if (wid == 0) {
         // ------------------------------ copies ------------------------------
@@ -265,9 +259,9 @@ gemm_i8_pair_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_const
             tile_at(p, t, mi, ni);
             const int64_t m0 = (int64_t)mi * kTile + rank * kHalf + quarter * 32, n0 = (int64_t)ni * kTile;
             named_bar_sync(1, 128);  // the scales of the tile before have been read
-            for (int i = et; i < kTile; i += 128) sw[i] = n0 + i < p.N ? bf16_to_f32(ld_nc_u16(p.ws + n0 + i)) : 0.0f;
+            for (int i = et; i < kTile; i += 128) sw[i] = n0 + i < p.N ? bf16_to_f32(p.ws[n0 + i]) : 0.0f;
             named_bar_sync(1, 128);
-            const float sx = m0 + lane < p.M ? __ldg(p.xs + m0 + lane) : 0.0f;
+            const float sx = m0 + lane < p.M ? p.xs[m0 + lane] : 0.0f;
             const uint32_t buf = n & 1u;
             if (!wait(&b.d_full[buf], (n >> 1) & 1u)) break;
             tc_fence_after();
@@ -285,7 +279,7 @@ gemm_i8_pair_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_const
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         const int j = 8 * e + 2 * i;
-                        g[i] = pack_bf16x2(__fmul_rn((float)(int)v[j], __fmul_rn(sx, sw[c + j])),
+                        g[i] = pack2_bf16(__fmul_rn((float)(int)v[j], __fmul_rn(sx, sw[c + j])),
                                            __fmul_rn((float)(int)v[j + 1], __fmul_rn(sx, sw[c + j + 1])));
                     }
                     *reinterpret_cast<uint4 *>(out + lane * 64 + (e ^ ((lane >> 1) & 3)) * 16) = make_uint4(g[0], g[1], g[2], g[3]);
@@ -410,7 +404,6 @@ gemm_i8_stream_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_con
     const int64_t beg = p.plan.begin_of(blockIdx.x), end = p.plan.end_of(blockIdx.x);
     auto wait = [&](uint64_t *bar, uint32_t parity) { return mbar_wait(bar, parity, p.g.status, &b.abort); };
 
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (tid == 0) {
         for (uint32_t i = 0; i < S; ++i) {
             mbar_init(&b.full[i], 1);
@@ -430,6 +423,8 @@ gemm_i8_stream_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_con
     tc_fence_after();
     const uint32_t tmem = b.tmem;
     asm volatile("griddepcontrol.wait;" ::: "memory");  // what came before on the stream is complete from here on
+    // not earlier: a next kernel that reads its weights before its own wait counts on all but this one being complete
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
     if (wid == 0) {
         // ------------------------------ copies ------------------------------
@@ -501,10 +496,10 @@ gemm_i8_stream_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_con
             const int s0 = (int)(u - tile * stages), s1 = (int)std::min<int64_t>(stages, s0 + (end - u));
             const int64_t nr = tile % nt * 128 + r, m0 = tile / nt * BN;
             const int cols = (int)std::min<int64_t>(BN, M - m0);
-            const float sw = nr < N ? bf16_to_f32(ld_nc_u16(p.g.ws + nr)) : 0.0f;
+            const float sw = nr < N ? bf16_to_f32(p.g.ws[nr]) : 0.0f;
             if (m0 != sx_at) {  // the tokens' scales, while the MMAs run
                 named_bar_sync(1, 128);
-                if (r < cols) b.sx[r] = __ldg(p.g.xs + m0 + r);
+                if (r < cols) b.sx[r] = p.g.xs[m0 + r];
                 named_bar_sync(1, 128);
                 sx_at = m0;
             }
@@ -606,7 +601,7 @@ gemm_i8_stream_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_con
                 const int *parts = p.part + tile * p.plan.max_segs * (BN * 128) + 4 * lane;
                 float sw[4];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) sw[i] = nr + i < N ? bf16_to_f32(ld_nc_u16(p.g.ws + nr + i)) : 0.0f;
+                for (int i = 0; i < 4; ++i) sw[i] = nr + i < N ? bf16_to_f32(p.g.ws[nr + i]) : 0.0f;
                 // a warp adds up one column of 128 rows at a time, 4 rows per lane
                 for (int c = c0 + quarter; c < c1; c += 4 * kColumns) {
                     int4 v[kColumns];
@@ -625,12 +620,12 @@ gemm_i8_stream_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_con
                     for (int i = 0; i < kColumns; ++i) {
                         if (c + 4 * i >= c1) continue;
                         const int64_t m = m0 + c + 4 * i;
-                        const float sx = __ldg(p.g.xs + m);
+                        const float sx = p.g.xs[m];
                         const float y0 = __fmul_rn((float)v[i].x, __fmul_rn(sx, sw[0])), y1 = __fmul_rn((float)v[i].y, __fmul_rn(sx, sw[1]));
                         const float y2 = __fmul_rn((float)v[i].z, __fmul_rn(sx, sw[2])), y3 = __fmul_rn((float)v[i].w, __fmul_rn(sx, sw[3]));
                         uint16_t *to = p.g.y + m * N + nr;
                         if (N % 4 == 0) {
-                            if (nr < N) *reinterpret_cast<uint2 *>(to) = make_uint2(pack_bf16x2(y0, y1), pack_bf16x2(y2, y3));
+                            if (nr < N) *reinterpret_cast<uint2 *>(to) = make_uint2(pack2_bf16(y0, y1), pack2_bf16(y2, y3));
                         } else {
                             if (nr < N) to[0] = f32_to_bf16(y0);
                             if (nr + 1 < N) to[1] = f32_to_bf16(y1);
@@ -780,7 +775,7 @@ int run_pairs(const int8_t *xq, const int8_t *wq, Args a, int sms, cudaStream_t 
     a.nt = (int)((a.N + kTile - 1) / kTile);
     a.band = (int)std::max<int64_t>(1, std::min<int64_t>(a.mt, kBandBytes / (kTile * a.K)));
     const int64_t pairs = std::min<int64_t>((int64_t)a.mt * a.nt, sms / 2);
-    gemm_i8_pair_kernel<<<(unsigned)(2 * pairs), kThreads, kSmem + 1024, st>>>(xmap, wmap, a);
+    launch_behind(gemm_i8_pair_kernel, (unsigned)(2 * pairs), kThreads, kSmem + 1024, st, xmap, wmap, a);
     return 0;
 }
 

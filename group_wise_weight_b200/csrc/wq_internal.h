@@ -24,6 +24,25 @@ inline cudaError_t clear_extra_counters(void *workspace, int64_t tiles, cudaStre
     return cudaMemsetAsync(static_cast<uint8_t *>(workspace) + kCounterRegion, 0, region - kCounterRegion, st);
 }
 
+// Launches `kernel` so that it may start while the previous kernel on the stream ends (programmatic dependent launch).  It
+// must wait for that one (griddepcontrol.wait) before it reads or writes anything, and let the next start no earlier.
+// A failure is the caller's last error.
+template <typename... P>
+void launch_behind(void (*kernel)(P...), unsigned grid, unsigned threads, size_t smem, cudaStream_t st, P... args)
+{
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 // y [M][N] bf16 overlaps x [M][K] bf16, the codes, the scales or the zero-points (wq_api.cu).
 bool output_overlaps_inputs(const void *x, int64_t M, int64_t N, int64_t K, const void *q, const void *s,
                             const void *z, int g, const void *y, bool int8);

@@ -22,13 +22,14 @@
 // (wq_quotient.cuh): one correction step for the bf16 scales of int4, two for
 // the arbitrary binary32 scale of fp8; blocks outside the proven range use
 // the IEEE division.
-// Measured, 16,000 tokens of 8 heads: fp8 20.7 us (4.7 TB/s), int4 25 us (3.3
-// TB/s); the schedulers issue 70% of the time, so the instructions bind.  The
+// Measured, 16,000 tokens of 8 heads: fp8 18.8 us (5.2 TB/s; 20.6 without the
+// launch while the previous kernel ends), int4 25 us (3.3 TB/s); the schedulers issue 70% of the time, so the instructions bind.  The
 // blocks of a lane are left to other warps (one vector per group of lanes):
 // several in turn per warp took 22.8 us.
 #include <algorithm>
 
 #include "wq_internal.h"
+#include "wq_prompt.cuh"
 #include "wq_quotient.cuh"
 
 namespace wq {
@@ -162,6 +163,8 @@ template <bool FP8>
 __global__ void __launch_bounds__(kThreads)
 kv_store_kernel(const StoreArgs p)
 {
+    asm volatile("griddepcontrol.wait;" ::: "memory");  // what came before on the stream is complete from here on
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const unsigned l = threadIdx.x % kLanes, H = (unsigned)p.H, j = blockIdx.x * kGroups + threadIdx.x / kLanes;
     int64_t slot = -1, row = 0;
     uint4 raw[2] = {make_uint4(0u, 0u, 0u, 0u), make_uint4(0u, 0u, 0u, 0u)};
@@ -170,15 +173,15 @@ kv_store_kernel(const StoreArgs p)
         const unsigned m = j / (2u * H), rest = j - m * 2u * H;
         is_v = rest >= H;
         const unsigned h = is_v ? rest - H : rest;
-        slot = __ldg(p.slots + m);
+        slot = p.slots[m];
         if (slot >= p.S) slot = -1;
         const uint16_t *src = (is_v ? p.v + m * p.ldv : p.k + m * p.ldk) + h * kD + l * 16;
-        raw[0] = ld_stream_v4(src);
-        raw[1] = ld_stream_v4(src + 8);
+        raw[0] = ld_written_v4(src);
+        raw[1] = ld_written_v4(src + 8);
         row = slot * H + h;
     }
     if (FP8) {
-        const uint4 c = fp8_codes(raw, __ldg(is_v ? p.v8s : p.k8s));
+        const uint4 c = fp8_codes(raw, *(is_v ? p.v8s : p.k8s));
         if (slot >= 0) *reinterpret_cast<uint4 *>((is_v ? p.vc : p.kc) + row * kD + l * 16) = c;
     } else {
         float s, z;
@@ -201,8 +204,8 @@ void launch_kv_store(bool fp8, const uint16_t *k, int64_t ldk, const uint16_t *v
 {
     const StoreArgs a{k, v, ldk, ldv, slots, M, S, (int)H, kc, vc, ks, kz, vs, vz, k8s, v8s};
     const unsigned grid = (unsigned)((M * 2 * H + kGroups - 1) / kGroups);
-    if (fp8) kv_store_kernel<true><<<grid, kThreads, 0, st>>>(a);
-    else kv_store_kernel<false><<<grid, kThreads, 0, st>>>(a);
+    if (fp8) launch_behind(kv_store_kernel<true>, grid, kThreads, 0, st, a);
+    else launch_behind(kv_store_kernel<false>, grid, kThreads, 0, st, a);
 }
 
 }  // namespace wq

@@ -38,7 +38,7 @@
 // one sequence of 16,384 tokens, 64 query and 8 KV heads of 128, 3.34 ms
 // (1,317 TFLOP/s; 3.94 ms once the power cap lowers the clock); 32 query heads
 // of 64, 1.35 ms (817).  Short prompts lose the ends: 48 of 1 to 331 tokens,
-// 64 query heads, 82 us.  A block of 64 keys with two S tiles, a polynomial for
+// 64 query heads, 76 us.  A block of 64 keys with two S tiles, a polynomial for
 // part of the exponentials, softmax warpgroups that take turns and key blocks
 // asked into L2 ahead each gained nothing.
 //
@@ -56,7 +56,7 @@
 #include <atomic>
 
 #include "wq_internal.h"
-#include "wq_sm100.cuh"
+#include "wq_prompt.cuh"
 
 namespace wq {
 
@@ -196,14 +196,6 @@ __device__ __forceinline__ void registers_dec() { asm volatile("setmaxnreg.dec.s
 template <int N>
 __device__ __forceinline__ void registers_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
 
-// One lane of the (whole) warp.
-__device__ __forceinline__ bool elect_one()
-{
-    uint32_t p;
-    asm volatile("{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\tselp.u32 %0, 1, 0, q;\n\t}" : "=r"(p));
-    return p != 0;
-}
-
 __device__ __forceinline__ float max3(float a, float b, float c)
 {
     float d;
@@ -296,6 +288,8 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_consta
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = b.tmem;
+    asm volatile("griddepcontrol.wait;" ::: "memory");  // what came before on the stream is complete from here on
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
     if (wid == kLoadWarp) {
         // ------------------------------ items and copies ------------------------------
@@ -539,7 +533,7 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_consta
                         const f32x2 y = fma2_pairs(s2, sc, sh);
                         const f32x2 q{ex2(y.x), ex2(y.y)};
                         sum[e & 1] = add2_pairs(sum[e & 1], q);
-                        w[e] = pack_bf16x2(q.x, q.y);
+                        w[e] = pack2_bf16(q.x, q.y);
                     }
                     tmem_st16(p_addr + 16u * c, w);
                 };
@@ -668,7 +662,7 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_consta
                         uint32_t g[4];
 #pragma unroll
                         for (int i = 0; i < 4; ++i)
-                            g[i] = pack_bf16x2(__uint_as_float(w[8 * e + 2 * i]) * inv, __uint_as_float(w[8 * e + 2 * i + 1]) * inv);
+                            g[i] = pack2_bf16(__uint_as_float(w[8 * e + 2 * i]) * inv, __uint_as_float(w[8 * e + 2 * i + 1]) * inv);
                         *reinterpret_cast<uint4 *>(out + lane * 64 + (e ^ ((lane >> 1) & 3)) * 16) = make_uint4(g[0], g[1], g[2], g[3]);
                     }
                     __syncwarp();
@@ -764,7 +758,7 @@ int run(const uint16_t *q, int64_t ldq, const uint16_t *k, int64_t ldk, const ui
         return -1;
     if (!prepare_device()) return -2;
     const unsigned grid = (unsigned)prompt_attention_items(a.M, a.B, a.r * (int64_t)a.H, a.H);
-    prompt_attn_kernel<D><<<grid, kThreads, Cfg<D>::kBytes + 1024, st>>>(qm, km, vm, a);
+    launch_behind(prompt_attn_kernel<D>, grid, kThreads, Cfg<D>::kBytes + 1024, st, qm, km, vm, a);
     return 0;
 }
 

@@ -25,6 +25,7 @@
 // Measured: 8,192 x 28,672 bf16 115 us (6.1 TB/s, 93% of a copy); one row of
 // 8,192 6.3 us, which is what the host needs to make the calls.
 #include "wq_internal.h"
+#include "wq_prompt.cuh"
 #include "wq_quotient.cuh"
 
 namespace wq {
@@ -42,7 +43,7 @@ __device__ __forceinline__ Raw8<T> load_raw(const T *p)
 {
     Raw8<T> r;
 #pragma unroll
-    for (int j = 0; j < (int)(sizeof(T) / 2); ++j) r.w[j] = ld_nc_v4(p + j * (16 / sizeof(T)));
+    for (int j = 0; j < (int)(sizeof(T) / 2); ++j) r.w[j] = ld_written_v4(p + j * (16 / sizeof(T)));
     return r;
 }
 
@@ -130,9 +131,11 @@ constexpr int kWarpRows = 8;  // rows (warps) per CTA of the short-row form
 // Rows of up to 256 CH values: one warp per row.
 template <typename T, int CH>
 __global__ void __launch_bounds__(kWarpRows * 32)
-quant_tokens_warp_kernel(const T *__restrict__ x, int64_t M, int64_t K, int64_t ldx, int8_t *__restrict__ q,
+quant_tokens_warp_kernel(const T *x, int64_t M, int64_t K, int64_t ldx, int8_t *__restrict__ q,
                          float *__restrict__ scales)
 {
+    asm volatile("griddepcontrol.wait;" ::: "memory");  // what came before on the stream is complete from here on
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int lane = threadIdx.x & 31;
     const int64_t m = (int64_t)blockIdx.x * kWarpRows + (threadIdx.x >> 5);
     if (m >= M) return;
@@ -172,9 +175,11 @@ __device__ __forceinline__ float cta_max(float v)
 // Rows of up to 8 THREADS CH values: one CTA per row, the row in registers.
 template <typename T, int THREADS, int CH>
 __global__ void __launch_bounds__(THREADS)
-quant_tokens_row_kernel(const T *__restrict__ x, int64_t K, int64_t ldx, int8_t *__restrict__ q,
+quant_tokens_row_kernel(const T *x, int64_t K, int64_t ldx, int8_t *__restrict__ q,
                         float *__restrict__ scales)
 {
+    asm volatile("griddepcontrol.wait;" ::: "memory");  // what came before on the stream is complete from here on
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int64_t m = blockIdx.x;
     const T *row = x + m * ldx;
     Raw8<T> v[CH];
@@ -200,9 +205,11 @@ quant_tokens_row_kernel(const T *__restrict__ x, int64_t K, int64_t ldx, int8_t 
 // Longer rows: the maximum, then a second pass over the row.
 template <typename T, int THREADS>
 __global__ void __launch_bounds__(THREADS)
-quant_tokens_long_kernel(const T *__restrict__ x, int64_t K, int64_t ldx, int8_t *__restrict__ q,
+quant_tokens_long_kernel(const T *x, int64_t K, int64_t ldx, int8_t *__restrict__ q,
                          float *__restrict__ scales)
 {
+    asm volatile("griddepcontrol.wait;" ::: "memory");  // what came before on the stream is complete from here on
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int64_t m = blockIdx.x;
     const T *row = x + m * ldx;
     float amax = 0.0f;
@@ -221,14 +228,14 @@ template <typename T>
 void dispatch(const T *x, int64_t M, int64_t K, int64_t ldx, int8_t *q, float *s, cudaStream_t st)
 {
     const unsigned rows = (unsigned)M, warps = (unsigned)((M + kWarpRows - 1) / kWarpRows);
-    if (K <= 512) quant_tokens_warp_kernel<T, 2><<<warps, kWarpRows * 32, 0, st>>>(x, M, K, ldx, q, s);
-    else if (K <= 1024) quant_tokens_warp_kernel<T, 4><<<warps, kWarpRows * 32, 0, st>>>(x, M, K, ldx, q, s);
-    else if (K <= 2048) quant_tokens_warp_kernel<T, 8><<<warps, kWarpRows * 32, 0, st>>>(x, M, K, ldx, q, s);
-    else if (K <= 4096) quant_tokens_row_kernel<T, 256, 2><<<rows, 256, 0, st>>>(x, K, ldx, q, s);
-    else if (K <= 8192) quant_tokens_row_kernel<T, 256, 4><<<rows, 256, 0, st>>>(x, K, ldx, q, s);
-    else if (K <= 16384) quant_tokens_row_kernel<T, 512, 4><<<rows, 512, 0, st>>>(x, K, ldx, q, s);
-    else if (K <= 32768) quant_tokens_row_kernel<T, 512, 8><<<rows, 512, 0, st>>>(x, K, ldx, q, s);
-    else quant_tokens_long_kernel<T, 512><<<rows, 512, 0, st>>>(x, K, ldx, q, s);
+    if (K <= 512) launch_behind(quant_tokens_warp_kernel<T, 2>, warps, kWarpRows * 32, 0, st, x, M, K, ldx, q, s);
+    else if (K <= 1024) launch_behind(quant_tokens_warp_kernel<T, 4>, warps, kWarpRows * 32, 0, st, x, M, K, ldx, q, s);
+    else if (K <= 2048) launch_behind(quant_tokens_warp_kernel<T, 8>, warps, kWarpRows * 32, 0, st, x, M, K, ldx, q, s);
+    else if (K <= 4096) launch_behind(quant_tokens_row_kernel<T, 256, 2>, rows, 256, 0, st, x, K, ldx, q, s);
+    else if (K <= 8192) launch_behind(quant_tokens_row_kernel<T, 256, 4>, rows, 256, 0, st, x, K, ldx, q, s);
+    else if (K <= 16384) launch_behind(quant_tokens_row_kernel<T, 512, 4>, rows, 512, 0, st, x, K, ldx, q, s);
+    else if (K <= 32768) launch_behind(quant_tokens_row_kernel<T, 512, 8>, rows, 512, 0, st, x, K, ldx, q, s);
+    else launch_behind(quant_tokens_long_kernel<T, 512>, rows, 512, 0, st, x, K, ldx, q, s);
 }
 
 }  // namespace

@@ -22,13 +22,16 @@
 // heads of a token:
 //   y_a = inv (a (w_a cos) - b (w_b sin)),  y_b = inv (b (w_b cos) + a (w_a sin)).
 // A warp takes 256 / D heads of one token at a time, kUnroll loads in flight;
-// where tokens are few a token's heads are shared out to several warps.
-// Measured: 16,384 tokens, 64 + 8 heads of 128 with norms, 103 us (5.8 TB/s,
-// 89% of a copy); 128 tokens 5 to 7 us, the launch and the latency of a load.
+// where tokens are few a token's heads are shared out to several warps, its
+// queries and keys apart.  The first heads' loads are under way while the
+// sines and cosines are formed, and the kernel starts while the previous one
+// ends (without the two 128 tokens took 7.3 us, 16,384 104).
+// Measured: 16,384 tokens, 64 + 8 heads of 128 with norms, 100 us (6.0 TB/s,
+// 92% of a copy); 128 tokens 5.7 us, 4.4 in a graph: launch and load latency.
 #include <algorithm>
 
-#include "wq_common.cuh"
 #include "wq_internal.h"
+#include "wq_prompt.cuh"
 
 namespace wq {
 
@@ -45,7 +48,7 @@ struct RopeArgs {
     const int32_t *positions;
     const float *inv_freq;
     float eps;
-    int half, Hq, H, split;  // split: warps per token
+    int half, Hq, H, split, qsplit;  // warps per token; with more than one, those of the queries (the others have the keys)
     uint16_t *qo, *ko;
 };
 
@@ -73,19 +76,44 @@ __device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b)
     return r;
 }
 
+// What a lane has in flight: its values of kUnroll heads.
+struct Batch {
+    uint2 u[kUnroll], v[kUnroll];
+};
+
 // The heads base + g, base + g + step, ... below `heads` of one token's queries (or keys), g the lane's group in the
 // warp: src and dst at the token's row; o1, o2 the places of this lane's two groups of 4 values in a head.
+template <int D, bool INTERLEAVED>
+__device__ __forceinline__ void load_heads(Batch &x, const uint16_t *src, int base, int g, int step, int heads, int o1, int o2)
+{
+#pragma unroll
+    for (int e = 0; e < kUnroll; ++e) {
+        const int h = base + g + e * step;
+        x.u[e] = x.v[e] = make_uint2(0u, 0u);
+        if (h < heads) {
+            if (INTERLEAVED) {
+                const uint4 r = *reinterpret_cast<const uint4 *>(src + h * D + o1);
+                x.u[e] = make_uint2(r.x, r.y);
+                x.v[e] = make_uint2(r.z, r.w);
+            } else {
+                x.u[e] = *reinterpret_cast<const uint2 *>(src + h * D + o1);
+                x.v[e] = *reinterpret_cast<const uint2 *>(src + h * D + o2);
+            }
+        }
+    }
+}
+
+// Turns them, `first` and the lane's weights w1, w2 being loaded already.
 template <int D, bool INTERLEAVED, bool NORM>
-__device__ __forceinline__ void turn_heads(const uint16_t *src, uint16_t *dst, int base, int g, int step, int heads,
-                                           int o1, int o2, const uint16_t *weight, const float c[4], const float s[4], float eps)
+__device__ __forceinline__ void turn_heads(Batch &first, const uint16_t *src, uint16_t *dst, int base, int g, int step, int heads,
+                                           int o1, int o2, uint2 w1, uint2 w2, const float c[4], const float s[4], float eps)
 {
     constexpr int L = D / 8;  // lanes per head
     float wa[4], wb[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) wa[i] = wb[i] = 1.0f;
     if (NORM) {
-        const Pairs w = unpack<INTERLEAVED>(__ldg(reinterpret_cast<const uint2 *>(weight + o1)),
-                                            __ldg(reinterpret_cast<const uint2 *>(weight + o2)));
+        const Pairs w = unpack<INTERLEAVED>(w1, w2);
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             wa[2 * i] = w.a[i].x; wa[2 * i + 1] = w.a[i].y;
@@ -100,27 +128,11 @@ __device__ __forceinline__ void turn_heads(const uint16_t *src, uint16_t *dst, i
         bc[i] = f32x2{wb[2 * i] * c[2 * i], wb[2 * i + 1] * c[2 * i + 1]};
         bs[i] = f32x2{-wb[2 * i] * s[2 * i], -wb[2 * i + 1] * s[2 * i + 1]};
     }
-    for (; base < heads; base += step * kUnroll) {
-        uint2 u[kUnroll], v[kUnroll];
+    while (base < heads) {
 #pragma unroll
         for (int e = 0; e < kUnroll; ++e) {
             const int h = base + g + e * step;
-            u[e] = v[e] = make_uint2(0u, 0u);
-            if (h < heads) {
-                if (INTERLEAVED) {
-                    const uint4 x = *reinterpret_cast<const uint4 *>(src + h * D + o1);
-                    u[e] = make_uint2(x.x, x.y);
-                    v[e] = make_uint2(x.z, x.w);
-                } else {
-                    u[e] = *reinterpret_cast<const uint2 *>(src + h * D + o1);
-                    v[e] = *reinterpret_cast<const uint2 *>(src + h * D + o2);
-                }
-            }
-        }
-#pragma unroll
-        for (int e = 0; e < kUnroll; ++e) {
-            const int h = base + g + e * step;
-            const Pairs x = unpack<INTERLEAVED>(u[e], v[e]);
+            const Pairs x = unpack<INTERLEAVED>(first.u[e], first.v[e]);
             f32x2 ya[2], yb[2];
             float inv = 1.0f;
             if (NORM) {
@@ -145,14 +157,16 @@ __device__ __forceinline__ void turn_heads(const uint16_t *src, uint16_t *dst, i
             if (h < heads) {
                 if (INTERLEAVED) {
                     *reinterpret_cast<uint4 *>(dst + h * D + o1) =
-                        make_uint4(pack_bf16x2(ya[0].x, yb[0].x), pack_bf16x2(ya[0].y, yb[0].y),
-                                   pack_bf16x2(ya[1].x, yb[1].x), pack_bf16x2(ya[1].y, yb[1].y));
+                        make_uint4(pack2_bf16(ya[0].x, yb[0].x), pack2_bf16(ya[0].y, yb[0].y),
+                                   pack2_bf16(ya[1].x, yb[1].x), pack2_bf16(ya[1].y, yb[1].y));
                 } else {
-                    *reinterpret_cast<uint2 *>(dst + h * D + o1) = make_uint2(pack_bf16x2(ya[0].x, ya[0].y), pack_bf16x2(ya[1].x, ya[1].y));
-                    *reinterpret_cast<uint2 *>(dst + h * D + o2) = make_uint2(pack_bf16x2(yb[0].x, yb[0].y), pack_bf16x2(yb[1].x, yb[1].y));
+                    *reinterpret_cast<uint2 *>(dst + h * D + o1) = make_uint2(pack2_bf16(ya[0].x, ya[0].y), pack2_bf16(ya[1].x, ya[1].y));
+                    *reinterpret_cast<uint2 *>(dst + h * D + o2) = make_uint2(pack2_bf16(yb[0].x, yb[0].y), pack2_bf16(yb[1].x, yb[1].y));
                 }
             }
         }
+        base += step * kUnroll;
+        if (base < heads) load_heads<D, INTERLEAVED>(first, src, base, g, step, heads, o1, o2);
     }
 }
 
@@ -166,17 +180,31 @@ qk_norm_rope_kernel(const RopeArgs p)
     const int64_t task = (int64_t)blockIdx.x * kWarps + wid;
     const int64_t m = task / p.split;
     const int part = (int)(task - m * p.split);
+    asm volatile("griddepcontrol.wait;" ::: "memory");  // what came before on the stream is complete from here on
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (m >= p.M) return;
+    // lane l holds the pairs 4 l .. 4 l + 3; past the rotated ones, 8 values that do not turn
+    const bool turned = 4 * l < p.half;
+    const int o1 = INTERLEAVED ? 8 * l : turned ? 4 * l : 8 * l;
+    const int o2 = INTERLEAVED ? 8 * l + 4 : turned ? p.half + 4 * l : 8 * l + 4;
+    // the first heads and their weights are on their way while the sines and cosines are formed
+    const bool keys = p.split > 1 && part >= p.qsplit;
+    const uint16_t *src = keys ? p.k + m * p.ldk : p.q + m * p.ldq, *weight = keys ? p.kw : p.qw;
+    const int base = (keys ? part - p.qsplit : part) * kHeads, step = (p.split == 1 ? 1 : keys ? p.split - p.qsplit : p.qsplit) * kHeads;
+    const int heads = keys ? p.H : p.Hq;
+    Batch first;
+    load_heads<D, INTERLEAVED>(first, src, base, g, step, heads, o1, o2);
+    uint2 w1 = make_uint2(0u, 0u), w2 = w1;
+    if (NORM) {
+        w1 = *reinterpret_cast<const uint2 *>(weight + o1);
+        w2 = *reinterpret_cast<const uint2 *>(weight + o2);
+    }
     const double pos = (double)p.positions[m];
     for (int f = lane; f < p.half; f += 32) {
         const double turns = pos * (double)p.inv_freq[f] * 0.15915494309189535;  // / 2 pi
         sincospif((float)(2.0 * (turns - rint(turns))), &table[wid][1][f], &table[wid][0][f]);
     }
     __syncwarp();
-    // lane l holds the pairs 4 l .. 4 l + 3; past the rotated ones, 8 values that do not turn
-    const bool turned = 4 * l < p.half;
-    const int o1 = INTERLEAVED ? 8 * l : turned ? 4 * l : 8 * l;
-    const int o2 = INTERLEAVED ? 8 * l + 4 : turned ? p.half + 4 * l : 8 * l + 4;
     float c[4] = {1.0f, 1.0f, 1.0f, 1.0f}, s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
     if (turned) {
         const float4 cv = *reinterpret_cast<const float4 *>(&table[wid][0][4 * l]);
@@ -184,17 +212,23 @@ qk_norm_rope_kernel(const RopeArgs p)
         c[0] = cv.x; c[1] = cv.y; c[2] = cv.z; c[3] = cv.w;
         s[0] = sv.x; s[1] = sv.y; s[2] = sv.z; s[3] = sv.w;
     }
-    const int step = p.split * kHeads;
-    turn_heads<D, INTERLEAVED, NORM>(p.q + m * p.ldq, p.qo + m * p.ldqo, part * kHeads, g, step, p.Hq, o1, o2, p.qw, c, s, p.eps);
-    // the keys from the other end, so that the warps with fewer query heads take them
-    turn_heads<D, INTERLEAVED, NORM>(p.k + m * p.ldk, p.ko + m * p.ldko, (p.split - 1 - part) * kHeads, g, step, p.H, o1, o2, p.kw, c, s, p.eps);
+    uint16_t *dst = keys ? p.ko + m * p.ldko : p.qo + m * p.ldqo;
+    turn_heads<D, INTERLEAVED, NORM>(first, src, dst, base, g, step, heads, o1, o2, w1, w2, c, s, p.eps);
+    if (p.split > 1) return;
+    src = p.k + m * p.ldk;
+    load_heads<D, INTERLEAVED>(first, src, 0, g, kHeads, p.H, o1, o2);
+    if (NORM) {
+        w1 = *reinterpret_cast<const uint2 *>(p.kw + o1);
+        w2 = *reinterpret_cast<const uint2 *>(p.kw + o2);
+    }
+    turn_heads<D, INTERLEAVED, NORM>(first, src, p.ko + m * p.ldko, 0, g, kHeads, p.H, o1, o2, w1, w2, c, s, p.eps);
 }
 
 template <int D, bool INTERLEAVED>
 void run(const RopeArgs &a, unsigned grid, cudaStream_t st)
 {
-    if (a.qw) qk_norm_rope_kernel<D, INTERLEAVED, true><<<grid, kThreads, 0, st>>>(a);
-    else qk_norm_rope_kernel<D, INTERLEAVED, false><<<grid, kThreads, 0, st>>>(a);
+    if (a.qw) launch_behind(qk_norm_rope_kernel<D, INTERLEAVED, true>, grid, kThreads, 0, st, a);
+    else launch_behind(qk_norm_rope_kernel<D, INTERLEAVED, false>, grid, kThreads, 0, st, a);
 }
 
 }  // namespace
@@ -204,10 +238,15 @@ void launch_qk_norm_rope(const uint16_t *q, int64_t ldq, const uint16_t *k, int6
                          int interleaved, int64_t M, int64_t Hq, int64_t H, int64_t D, uint16_t *qo, int64_t ldqo,
                          uint16_t *ko, int64_t ldko, cudaStream_t st)
 {
-    RopeArgs a{q, k, qw, kw, ldq, ldk, ldqo, ldko, M, positions, inv_freq, eps, (int)(rot / 2), (int)Hq, (int)H, 1, qo, ko};
-    // one warp per token once that fills the device (148 SMs x 32 warps), else a token's heads over more of them
-    const int64_t at_once = 256 / D, turns = (Hq + at_once - 1) / at_once;
-    a.split = (int)std::max<int64_t>(1, std::min<int64_t>(turns, 148 * 32 / M));
+    RopeArgs a{q, k, qw, kw, ldq, ldk, ldqo, ldko, M, positions, inv_freq, eps, (int)(rot / 2), (int)Hq, (int)H, 1, 1, qo, ko};
+    // one warp per token once that fills the device (148 SMs x 32 warps), else a token's heads over more of them, queries
+    // and keys apart
+    const int64_t at_once = 256 / D, room = 148 * 32 / M, qturns = (Hq + at_once - 1) / at_once, kturns = (H + at_once - 1) / at_once;
+    if (room >= 2) {
+        const int64_t kwarps = std::max<int64_t>(1, std::min(kturns, room * H / (Hq + H)));
+        a.qsplit = (int)std::min(qturns, room - kwarps);
+        a.split = a.qsplit + (int)kwarps;
+    }
     const unsigned grid = (unsigned)((M * a.split + kWarps - 1) / kWarps);
     if (D == 128) {
         if (interleaved) run<128, true>(a, grid, st);

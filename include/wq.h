@@ -478,6 +478,12 @@ int wq_gemm_w4a16_noalloc(const uint16_t *x, int64_t M, int64_t N, int64_t K, co
                           const uint16_t *scales, const uint16_t *zeros, int g, uint16_t *y, void *stream);
 
 /*
+ * The calls from here to wq_prompt_attention are launched with programmatic
+ * dependent launch: they start while the previous kernel on the stream ends,
+ * read and write nothing before it has completed, and let the next kernel
+ * start no earlier, so that for a call that reads its weights early they are
+ * the operation between the quantiser and it.
+ *
  * Symmetric INT8 quantisation of activations with one binary32 scale per row
  * (token): the left operand of wq_gemm_w8a8_int8  ([P3] "What quantisation
  * does", the scale dynamic and per token).
@@ -516,9 +522,7 @@ size_t wq_gemm_w8a8_int8_workspace_bytes(int64_t M, int64_t N, int64_t K);
  * Kernels, chosen by a model of their times: one that streams the weights
  * (128 of their rows by up to 128 tokens per tile, a tile's K cut between CTAs
  * where that pays), and for many tokens one that computes 256 x 256 tiles on
- * pairs of SMs and needs no workspace.  The streaming kernel is launched with
- * programmatic dependent launch, reads and writes nothing before the previous
- * kernel on the stream has completed, and runs at most one CTA per SM; where
+ * pairs of SMs and needs no workspace.  Both run at most one CTA per SM; where
  * the CTAs of a cut tile wait for one another's sums the launch is a
  * cooperative one, so that calls on several streams never hold the SMs that
  * the other waits for (every wait is bounded all the same).

@@ -145,3 +145,28 @@ def test_matmuls_whose_parts_wait_on_streams_of_two_priorities():
     for s in range(len(streams)):
         for i, y in enumerate(got[s]):
             assert torch.equal(y, jobs[(i + s) % len(jobs)][4])
+
+
+def test_weights_made_two_calls_before_a_kernel_that_reads_them_early():
+    """wq_gemm_w4a16 may read its weights before the call just before it has ended, so another call goes between the
+    quantiser and it: the INT8 matmul, which starts early itself, must be such a call."""
+    g = torch.Generator(device="cuda").manual_seed(8)
+    N, K = 28672, 8192
+    w = [torch.randn(N, K, generator=g, device="cuda").to(torch.bfloat16) for _ in range(2)]
+    x = torch.randn(1, K, generator=g, device="cuda").to(torch.bfloat16)
+    a, sx = wq.wq_quantize_int8_tokens(x[:, :512].contiguous())
+    small = torch.randint(-127, 128, (64, 512), generator=g, device="cuda", dtype=torch.int8)
+    sw = torch.ones(64, device="cuda", dtype=torch.bfloat16)
+    want = []
+    for t in w:
+        q, s, z = wq.wq_quantize_int4(t, 128)
+        torch.cuda.synchronize()
+        want.append(wq.wq_gemm_w4a16(x, q, s, z, 128))
+    torch.cuda.synchronize()
+    assert not torch.equal(want[0], want[1])
+    space = torch.zeros(wq.wq_gemm_workspace_bytes(1, N, K, 128, 4), dtype=torch.uint8, device="cuda")
+    torch.cuda.synchronize()
+    for i in range(10):
+        wq.wq_quantize_int4(w[i % 2], 128, qweight=q, scales=s, zeros=z)
+        wq.wq_gemm_w8a8_int8(a, sx, small, sw)
+        assert torch.equal(wq.wq_gemm_w4a16(x, q, s, z, 128, workspace=space), want[i % 2])
