@@ -17,6 +17,7 @@
 
 #include <ATen/ATen.h>
 #include <ATen/cuda/CUDAContext.h>
+#include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -79,7 +80,7 @@ void *dense(PyObject *o, const char *name, at::ScalarType type, at::IntArrayRef 
 void *output(PyObject *o, const char *name, at::ScalarType type, at::IntArrayRef shape, const at::Tensor &like, PyObject **ref)
 {
     if (o == Py_None) {
-        at::Tensor t = at::empty(shape, like.options().dtype(type));
+        at::Tensor t = at::detail::empty_cuda(shape, type, like.device(), std::nullopt);  // at::empty without its dispatch
         void *p = t.data_ptr();
         *ref = THPVariable_Wrap(std::move(t));
         if (!*ref) throw Refused();
