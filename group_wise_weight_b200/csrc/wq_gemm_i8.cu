@@ -6,27 +6,38 @@
 // AWQ, FP8, FP4 and KV-Cache Quantization", section "What quantisation does":
 // the product of the codes, scaled; here a scale per token and per channel).
 //
-// Two kernels, both persistent, both fed by TMA with the 128-byte swizzle in
+// Three kernels, all persistent, all fed by TMA with the 128-byte swizzle in
 // stages of 128 bytes of K (past K's end a copy fills in zeros, which add
 // nothing), accumulators double-buffered in tensor memory, every barrier wait
-// bounded (but the pair's two cluster barriers, which every thread reaches).
+// bounded (but a pair's two cluster barriers, which every thread reaches).
 //
-// Few rows (gemm_i8_stream_kernel): the weights are read once and bound the
-// call, so the work is cut along K as well: units of (tile, stage) in tile
-// order, dealt evenly over the SMs, or whole tiles where that is quicker.  A
-// tile is 128 weight rows (the MMA's M, so a token costs one of its N columns)
-// by 16 to 128 tokens.  A CTA that holds part of a tile leaves its integer
-// sums in the workspace and adds its stages to the tile's counter.  With few
-// parts and tokens the one that completes the counter adds the parts up
-// (exact, so in any order) and writes y; with more, every CTA of the tile
-// comes back at the end of its units, waits for the counter (bounded, and the
-// launch is cooperative: the parts of others never wait for this) and does a
-// share of the columns.  The
+// Few and middling rows (gemm_i8_rows_kernel): the weights bound the call, so
+// their rows are shared out evenly, rounded up to 8: up to 128 tokens N / 148 of
+// them to an SM (in rounds of at most 128), beyond that tiles of up to 128
+// tokens, the ones on the same weights next to one another; no sum is split.  A pair of CTAs
+// computes 128 tokens by twice that many weight rows: each loads its weight
+// rows and half of the tokens, which halves what the tokens take of an SM's
+// intake, and the pair's MMA (128 x up to 256) reads both halves.  Stages hold
+// several pieces of 128 bytes of K, as many as leave 5 stages in the ring: a
+// weight row's bytes then come in runs of up to 1 KB, which DRAM gives faster
+// (M = 1, 8192 x 28672: pieces singly 52.3 us, two 39.5, four 38.6; N = 1000:
+// 50.2, 32, 21).  Measured: M = 1, 10240 x 8192 17.4 us (4.8 TB/s); 8192 x 28672
+// 38.9 (6.0); M = 100, the same 43.3 us; M = 384, 2048 x 8192 11.5 us.  With the
+// other two kernels: 18.9, 39.8, 51.6, 20.9.
+//
+// Few weight rows and a deep K, or few rows and a shallow one
+// (gemm_i8_stream_kernel): tiles of 128 weight rows (the MMA's M, so a token
+// costs one of its N columns) by 16 to 128 tokens, whole ones to a CTA or a
+// tile's K in equal parts to several.  A CTA with a part leaves its integer sums
+// in the workspace and adds its stages to the tile's counter, waits for the
+// counter (bounded, and the launch is cooperative: CTAs that wait for one
+// another all run) and does a share of the columns, exact in any order.  The
 // ring takes 200 KB: what an SM has in flight sets the rate (M = 1, N = 57344,
-// K = 8192: 6 stages of 18 KB 81.6 us, 11 stages 72.8 us, 6.45 TB/s).  The kernel
-// is launched to set up while the previous one ends (0.4 us of a call; asking
-// L2 for its first weights then gained nothing) and reads and writes nothing
-// before that has completed.
+// K = 8192: 6 stages of 18 KB 81.6 us, 11 stages 72.8 us, 6.45 TB/s).
+//
+// All start while the previous kernel ends (0.4 us of a call; asking L2 for
+// the first weights then gained nothing) and read and write nothing before
+// that has completed.
 //
 // Many rows (gemm_i8_pair_kernel): the tensor cores bound the product, provided
 // the operands reach them: at 8,192 int8 multiply-adds per cycle an SM that
@@ -44,7 +55,6 @@
 // once the power cap lowers the clock); 2,048 x 8,192 x 8,192 94 us.
 #include <algorithm>
 #include <atomic>
-#include <type_traits>
 
 #include "wq_internal.h"
 #include "wq_prompt.cuh"
@@ -116,7 +126,7 @@ __device__ __forceinline__ void load_pair(void *dst, const CUtensorMap *map, uin
                  : "memory");
 }
 
-// D (+)= A B^T over the pair: 256 x 256, signed bytes, 32 of K.
+// D (+)= A B^T over the pair, signed bytes, 32 of K.
 __device__ __forceinline__ void mma_pair(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc, uint32_t accumulate)
 {
     asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
@@ -146,6 +156,44 @@ __device__ __forceinline__ void tile_at(const Args &p, int t, int &mi, int &ni)
     const int rows = min(p.band, p.mt - b * p.band);
     ni = rest / rows;
     mi = b * p.band + rest - ni * rows;
+}
+
+// 32 sums of this lane's row, scaled, to `to` (row 0's place; rows N apart): `rows` rows and `cols` columns of them, 16 bytes
+// at a time where `vectors` says that the places allow it.  A warp's 32 rows go through `out`, so that a store
+// instruction writes 8 rows' 64 adjacent bytes.
+__device__ __forceinline__ void write_rows(const uint32_t v[32], float sx, const float *sw, uint8_t *out, uint16_t *to, int64_t N,
+                                           int rows, int cols, bool vectors)
+{
+    const int lane = threadIdx.x & 31;
+    // 16-byte pieces at piece ^ (row / 2) % 4 of the row's 64 bytes: no bank conflicts either way
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        uint32_t g[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int j = 8 * e + 2 * i;
+            g[i] = pack2_bf16(__fmul_rn((float)(int)v[j], __fmul_rn(sx, sw[j])),
+                              __fmul_rn((float)(int)v[j + 1], __fmul_rn(sx, sw[j + 1])));
+        }
+        *reinterpret_cast<uint4 *>(out + lane * 64 + (e ^ ((lane >> 1) & 3)) * 16) = make_uint4(g[0], g[1], g[2], g[3]);
+    }
+    __syncwarp();
+    if (vectors) {
+        const int piece = lane & 3;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int r = 8 * i + (lane >> 2);
+            const uint4 g = *reinterpret_cast<const uint4 *>(out + r * 64 + (piece ^ ((r >> 1) & 3)) * 16);
+            if (r < rows && 8 * piece < cols) *reinterpret_cast<uint4 *>(to + r * N + 8 * piece) = g;
+        }
+    } else {  // rows of y begin at any even address: one value per lane
+        for (int r = 0; r < rows; ++r) {
+            const int piece = (lane >> 3) ^ ((r >> 1) & 3);
+            const uint16_t h = *reinterpret_cast<const uint16_t *>(out + r * 64 + piece * 16 + (lane & 7) * 2);
+            if (lane < cols) to[r * N + lane] = h;
+        }
+    }
+    __syncwarp();
 }
 
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
@@ -272,36 +320,7 @@ gemm_i8_pair_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_const
                 uint32_t v[32];
                 tmem_ld32(tmem + lane_bits + buf * 256u + (uint32_t)c, v);
                 tmem_wait_ld();
-                // 16-byte pieces at piece ^ (row / 2) % 4 of the row's 64 bytes: no bank conflicts either way
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    uint32_t g[4];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int j = 8 * e + 2 * i;
-                        g[i] = pack2_bf16(__fmul_rn((float)(int)v[j], __fmul_rn(sx, sw[c + j])),
-                                           __fmul_rn((float)(int)v[j + 1], __fmul_rn(sx, sw[c + j + 1])));
-                    }
-                    *reinterpret_cast<uint4 *>(out + lane * 64 + (e ^ ((lane >> 1) & 3)) * 16) = make_uint4(g[0], g[1], g[2], g[3]);
-                }
-                __syncwarp();
-                if (vectors) {
-                    const int piece = lane & 3;
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int r = 8 * i + (lane >> 2);
-                        const uint4 g = *reinterpret_cast<const uint4 *>(out + r * 64 + (piece ^ ((r >> 1) & 3)) * 16);
-                        if (r < rows && c + 8 * piece < cols)
-                            *reinterpret_cast<uint4 *>(p.y + (m0 + r) * p.N + n0 + c + 8 * piece) = g;
-                    }
-                } else {  // rows of y begin at any even address: one value per lane
-                    for (int r = 0; r < rows; ++r) {
-                        const int piece = (lane >> 3) ^ ((r >> 1) & 3);
-                        const uint16_t h = *reinterpret_cast<const uint16_t *>(out + r * 64 + piece * 16 + (lane & 7) * 2);
-                        if (c + lane < cols) p.y[(m0 + r) * p.N + n0 + c + lane] = h;
-                    }
-                }
-                __syncwarp();
+                write_rows(v, sx, sw + c, out, p.y + m0 * p.N + n0 + c, p.N, rows, cols - c, vectors);
             }
             tc_fence_before();
             __syncwarp();
@@ -314,6 +333,180 @@ gemm_i8_pair_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_const
     cluster_sync();  // the peer's MMAs have read this CTA's shared memory, its arrivals have landed
     tc_fence_after();
     if (wid == 1) asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u) : "memory");
+}
+
+// ------------------------------------------------------------------------------------------------------------
+// The weights' rows shared out
+// ------------------------------------------------------------------------------------------------------------
+
+constexpr int kRowsStages = 24;               // at most
+constexpr int kRowsRing = 200 * 1024;
+constexpr int kLeastStages = 5;  // in the ring, before a stage takes more pieces of K
+constexpr int kRowsOut = kRowsRing + 8192;    // (the MMA reads 64 rows of tokens, stale ones behind the last stage's too)
+constexpr int kRowsScale = kRowsOut + 4 * kOutBytes;
+constexpr int kRowsBar = kRowsScale + 256 * 4;
+constexpr int kRowsSmem = kRowsBar + 512;
+
+struct RowsBars {
+    uint64_t full[kRowsStages], empty[kRowsStages], d_full[2], d_empty[2], done;
+    int abort;
+    uint32_t tmem;
+};
+static_assert(sizeof(RowsBars) <= 512, "the barrier area");
+
+struct RowsArgs {
+    Args g;
+    int tiles, mt;       // of 2 `each` weight rows by 2 `tokens` tokens; tiles of tokens, which vary first
+    int each, tokens;    // weight rows and tokens per CTA of a pair and tile
+    int token_bytes, weight_bytes, stage_bytes, stages;  // of 128 of K; PIECES of them to a stage
+};
+
+template <int PIECES>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+gemm_i8_rows_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CUtensorMap wmap, const RowsArgs a)
+{
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
+    RowsBars &b = *reinterpret_cast<RowsBars *>(smem + kRowsBar);
+    const Args &p = a.g;
+    const int tid = threadIdx.x, wid = tid >> 5, lane = tid & 31;
+    const uint32_t rank = cluster_rank(), S = (uint32_t)a.stages;
+    const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+    constexpr int kStep = PIECES * kRowBytes;  // of K
+    const int steps = (int)((p.K + kStep - 1) / kStep);
+    const bool other = a.tokens < p.M;  // the second CTA has tokens too (all but M = 1)
+    auto wait = [&](uint64_t *bar, uint32_t parity) { return mbar_wait(bar, parity, p.status, &b.abort); };
+
+    if (tid == 0) {
+        for (uint32_t i = 0; i < S; ++i) {
+            mbar_init(&b.full[i], 1);
+            mbar_init(&b.empty[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&b.d_full[i], 1);
+            mbar_init(&b.d_empty[i], 8);  // 4 epilogue warps of each CTA
+        }
+        mbar_init(&b.done, 1);
+        b.abort = 0;
+        fence_mbar_init();
+    }
+    if (wid == 1) {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&b.tmem)), "r"(256u) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    }
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync();
+    tc_fence_after();
+    const uint32_t tmem = b.tmem;
+    asm volatile("griddepcontrol.wait;" ::: "memory");  // what came before on the stream is complete from here on
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+
+    if (wid == 0) {
+        // ------------------------------ copies ------------------------------
+        if (elect_one()) {
+            uint32_t slot = 0, phase = 0, issued = 0;
+            const uint32_t bytes = (uint32_t)(2 * a.each + (other ? 2 : 1) * a.tokens) * kStep;  // both CTAs'
+            bool ok = true;
+            for (int t = pair; ok && t < a.tiles; t += pairs) {
+                const int n = (2 * (t / a.mt) + (int)rank) * a.each, m = (2 * (t % a.mt) + (int)rank) * a.tokens;
+                for (int s = 0; s < steps; ++s) {
+                    if (issued >= S && !wait(&b.empty[slot], phase ^ 1u)) { ok = false; break; }
+                    uint8_t *st = smem + slot * a.stage_bytes;
+                    if (rank == 0) mbar_arrive_expect_tx(&b.full[slot], bytes);
+                    const uint32_t bar = at_leader(&b.full[slot]);
+#pragma unroll
+                    for (int h = 0; h < PIECES; ++h) load_pair(st + PIECES * a.token_bytes + h * a.weight_bytes, &wmap, bar, s * kStep + h * kRowBytes, n);
+                    if (rank == 0 || other) {
+#pragma unroll
+                        for (int h = 0; h < PIECES; ++h) load_pair(st + h * a.token_bytes, &xmap, bar, s * kStep + h * kRowBytes, m);
+                    }
+                    ++issued;
+                    if (++slot == S) { slot = 0; phase ^= 1u; }
+                }
+            }
+            // the leader sees every copy of the pair land before either CTA may exit (bounded, ignoring abort)
+            if (rank == 0) {
+                for (uint32_t j = issued > S ? issued - S : 0; j < issued; ++j) {
+                    const uint64_t t0 = global_ns();
+                    while (!mbar_try_wait(&b.full[j % S], (j / S) & 1u))
+                        if (global_ns() - t0 > kWaitLimitNs) { record_timeout(p.status); break; }
+                }
+            }
+        }
+        __syncwarp();
+    } else if (wid == 1) {
+        // ------------------------------ MMAs: one thread of the leader ------------------------------
+        if (rank == 0 && elect_one()) {
+            uint32_t slot = 0, phase = 0, n = 0;
+            const uint32_t base = smem_u32(smem);
+            const uint32_t idesc = idesc_s8_s32(128, 2 * ((a.each + 15) & ~15));
+            bool ok = true;
+            for (int t = pair; ok && t < a.tiles; t += pairs, ++n) {
+                const uint32_t buf = n & 1u;
+                if (n >= 2 && !wait(&b.d_empty[buf], ((n >> 1) - 1) & 1u)) break;
+                tc_fence_after();
+                for (int s = 0; s < steps; ++s) {
+                    if (!wait(&b.full[slot], phase)) { ok = false; break; }
+                    tc_fence_after();
+                    const uint32_t x = base + slot * a.stage_bytes, w = x + PIECES * a.token_bytes;
+#pragma unroll
+                    for (int e = 0; e < 4 * PIECES; ++e)
+                        mma_pair(tmem + buf * 128u, smem_desc(x + e / 4 * a.token_bytes + 32u * (e % 4), 16, 1024, 2),
+                                 smem_desc(w + e / 4 * a.weight_bytes + 32u * (e % 4), 16, 1024, 2), idesc, (s > 0 || e > 0) ? 1u : 0u);
+                    commit_pair(&b.empty[slot]);
+                    if (++slot == S) { slot = 0; phase ^= 1u; }
+                }
+                if (ok) commit_pair(&b.d_full[buf]);
+            }
+            commit_pair(&b.done);
+            const uint64_t t0 = global_ns();
+            while (!mbar_try_wait(&b.done, 0))  // every MMA must complete before tensor memory is released
+                if (global_ns() - t0 > kWaitLimitNs) { record_timeout(p.status); break; }
+        }
+        __syncwarp();
+    } else {
+        // ------------------------------ epilogue: one token per thread ------------------------------
+        // Tensor memory holds the CTA's 64 tokens twice: lanes 0-63 with the first CTA's weight rows, 64-127 with the second's.
+        const int quarter = wid & 3, half = quarter >> 1, et = tid - 64;
+        const uint32_t lane_bits = (uint32_t)(quarter * 32) << 16;
+        uint8_t *out = smem + kRowsOut + (wid - 2) * kOutBytes;
+        float *sw = reinterpret_cast<float *>(smem + kRowsScale);
+        const uint32_t d_empty[2] = {at_leader(&b.d_empty[0]), at_leader(&b.d_empty[1])};
+        const bool vectors = p.N % 8 == 0;  // so is `each`
+        const int row = (quarter & 1) * 32;
+        uint32_t n = 0;
+        for (int t = pair; t < a.tiles; t += pairs, ++n) {
+            const int64_t first = 2 * (int64_t)(t / a.mt) * a.each, m0 = (int64_t)(2 * (t % a.mt) + (int)rank) * a.tokens + row;
+            const int rows = (int)min((int64_t)min(32, a.tokens - row), p.M - m0);
+            const float sx = lane < rows ? p.xs[m0 + lane] : 0.0f;
+            named_bar_sync(1, 128);  // the scales of the tile before have been read
+            for (int i = et; i < 2 * a.each; i += 128)
+                sw[i < a.each ? i : 128 + i - a.each] = first + i < p.N ? bf16_to_f32(p.ws[first + i]) : 0.0f;
+            named_bar_sync(1, 128);
+            const uint32_t buf = n & 1u;
+            if (!wait(&b.d_full[buf], (n >> 1) & 1u)) break;
+            tc_fence_after();
+            const int64_t n0 = first + half * a.each;
+            const int cols = (int)min((int64_t)a.each, p.N - n0);
+#pragma unroll 1
+            for (int c = 0; c < cols && rows > 0; c += 32) {
+                uint32_t v[32];
+                tmem_ld32(tmem + lane_bits + buf * 128u + (uint32_t)c, v);
+                tmem_wait_ld();
+                write_rows(v, sx, sw + 128 * half + c, out, p.y + m0 * p.N + n0 + c, p.N, rows, cols - c, vectors);
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) arrive_at(d_empty[buf]);
+        }
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync();  // the peer's MMAs have read this CTA's shared memory, its arrivals have landed
+    tc_fence_after();
+    if (wid == 1) asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(256u) : "memory");
 }
 
 // ------------------------------------------------------------------------------------------------------------
@@ -352,37 +545,26 @@ __device__ __forceinline__ int ld_acquire(const int *p)
 
 struct StreamBars {
     uint64_t full[11], empty[11], d_full[2], d_empty[2], done;
-    int abort, last;
+    int abort, complete;
     uint32_t tmem;
     float sx[128];
 };
 static_assert(sizeof(StreamBars) <= 1024, "the barrier area");
 
-// Units (tile, stage) in tile order, dealt to the CTAs in one of two ways.  split > 0: a tile's stages to `split` CTAs, `per`
-// to each (the last takes what is left), so that a CTA has one part of one tile.  split = 0: `per` to every CTA, the first
-// `extra` one more, the last what is left, wherever the tiles end.
+// Units (tile, stage) in tile order, `per` to a CTA: the stages of whole tiles where split = 1; else a tile's stages go to
+// `split` CTAs (the last takes what is left), so that a CTA has one part of one tile.
 struct Plan {
-    int64_t tiles, total;
-    int nt, stages, grid, split, per, extra, max_segs;
-    bool shared;  // who adds up a split tile: its CTAs, a share of the columns each, or the last of them to finish
+    int64_t tiles;
+    int nt, stages, grid, split, per;
     __host__ __device__ int64_t begin_of(int b) const
     {
-        if (split > 0) return (int64_t)(b / split) * stages + min_of((b % split) * per, stages);
-        return min_of((int64_t)b * per + (b < extra ? b : extra), total);
+        return split > 1 ? (int64_t)(b / split) * stages + b % split * per : (int64_t)b * per;
     }
     __host__ __device__ int64_t end_of(int b) const
     {
-        if (split > 0) return (int64_t)(b / split) * stages + min_of((b % split + 1) * per, stages);
-        return begin_of(b + 1);
+        const int64_t end = begin_of(b) + per, last = split > 1 ? (int64_t)(b / split + 1) * stages : tiles * stages;
+        return end < last ? end : last;
     }
-    __host__ __device__ int cta_of(int64_t u) const
-    {
-        if (split > 0) return (int)(u / stages) * split + (int)(u % stages) / per;
-        const int64_t big = (int64_t)extra * (per + 1);
-        return (int)(u < big ? u / (per + 1) : extra + (u - big) / per);
-    }
-    template <typename T>
-    static __host__ __device__ T min_of(T a, T b) { return a < b ? a : b; }
 };
 
 struct StreamArgs {
@@ -402,6 +584,7 @@ gemm_i8_stream_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_con
     StreamBars &b = *reinterpret_cast<StreamBars *>(smem + C::kBarOff);
     const int tid = threadIdx.x, wid = tid >> 5, lane = tid & 31, stages = p.plan.stages, nt = p.plan.nt;
     const int64_t beg = p.plan.begin_of(blockIdx.x), end = p.plan.end_of(blockIdx.x);
+    const int count = p.plan.split, mine = (int)blockIdx.x % count;  // parts of a tile, this CTA's
     auto wait = [&](uint64_t *bar, uint32_t parity) { return mbar_wait(bar, parity, p.g.status, &b.abort); };
 
     if (tid == 0) {
@@ -506,51 +689,26 @@ gemm_i8_stream_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_con
             if (!wait(&b.d_full[n & 1u], (n >> 1) & 1u)) { ok = false; break; }
             tc_fence_after();
             const uint32_t d = tmem + lane_bits + (n & 1u) * (uint32_t)BN;
-            const bool whole = s0 == 0 && s1 == stages;
-            // the tile's parts: [part][column][row]
-            int *parts = p.part + tile * p.plan.max_segs * (BN * 128);
-            const int first = p.plan.cta_of(tile * stages), mine = (int)blockIdx.x - first;
-            const int count = whole ? 1 : p.plan.cta_of(tile * stages + stages - 1) - first + 1;
-            bool writes = false;  // shared tiles are written below
-            if (!whole) {
+            if (count > 1) {  // the sums to the tile's parts: [part][column][row]
+                int *part = p.part + (tile * count + mine) * (BN * 128) + r;
 #pragma unroll 1
                 for (int c = 0; c < cols; c += 16) {
                     uint32_t v[16];
                     tmem_ld16(d + (uint32_t)c, v);
                     tmem_wait_ld();
-                    int *to = parts + ((int64_t)mine * BN + c) * 128 + r;
 #pragma unroll
                     for (int e = 0; e < 16; ++e)
-                        if (c + e < cols) to[e * 128] = (int)v[e];
+                        if (c + e < cols) part[(c + e) * 128] = (int)v[e];
                 }
                 __threadfence();
                 named_bar_sync(1, 128);
-                if (p.plan.shared) {
-                    if (tid == 64) atomicAdd(p.counters + tile, s1 - s0);
-                } else {
-                    if (tid == 64) b.last = atomicAdd(p.counters + tile, s1 - s0) + (s1 - s0) == stages;
-                    named_bar_sync(1, 128);
-                    writes = *(volatile int *)&b.last != 0;
-                    if (writes) __threadfence();
-                }
-            }
-            // 16 columns of this row, the other parts' sums added where there are any (whole tiles have their own copy of
-            // the loop: with the parts in it they took 40% longer)
-            auto write = [&](auto parted) {
+                if (tid == 64) atomicAdd(p.counters + tile, s1 - s0);
+            } else {
 #pragma unroll 1
                 for (int c = 0; c < cols; c += 16) {
                     uint32_t v[16];
                     tmem_ld16(d + (uint32_t)c, v);
                     tmem_wait_ld();
-                    if constexpr (decltype(parted)::value) {
-                        for (int o = 0; o < count; ++o) {
-                            if (o == mine) continue;
-                            const int *from = parts + ((int64_t)o * BN + c) * 128 + r;
-#pragma unroll
-                            for (int e = 0; e < 16; ++e)
-                                if (c + e < cols) v[e] += (uint32_t)__ldcg(from + e * 128);
-                        }
-                    }
                     if (nr < N) {
                         uint16_t *to = p.g.y + (m0 + c) * N + nr;
 #pragma unroll
@@ -560,45 +718,35 @@ gemm_i8_stream_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_con
                         }
                     }
                 }
-            };
-            if (whole) {
-                write(std::false_type{});
-            } else if (writes) {
-                write(std::true_type{});
-                if (tid == 64) p.counters[tile] = 0;  // every part has been counted: nobody else touches it
             }
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&b.d_empty[n & 1u]);
             u += s1 - s0;
         }
-        if (p.plan.shared && ok) {
-            // the split tiles, first and last of this CTA's range: its share of their columns
-            for (int e = 0; e < 2; ++e) {
-                const int64_t tile = (e == 0 ? beg : end - 1) / stages;
-                const int64_t t0 = tile * stages, t1 = t0 + stages;
-                if ((t0 >= beg && t1 <= end) || (e == 1 && t0 <= beg)) continue;  // whole, or done as the first
-                const int first = p.plan.cta_of(t0), mine = (int)blockIdx.x - first, count = p.plan.cta_of(t1 - 1) - first + 1;
-                if (tid == 64) {
-                    int there = 1;
-                    const uint64_t since = global_ns();
-                    while ((ld_acquire(p.counters + tile) & (kReader - 1)) != stages) {
-                        if (b.abort) { there = 0; break; }
-                        if (global_ns() - since > kWaitLimitNs) {
-                            record_timeout(p.g.status);
-                            b.abort = 1;
-                            there = 0;
-                            break;
-                        }
+        if (count > 1 && ok) {
+            // this CTA's share of its tile's columns
+            const int64_t tile = beg / stages;
+            if (tid == 64) {
+                int there = 1;
+                const uint64_t since = global_ns();
+                while ((ld_acquire(p.counters + tile) & (kReader - 1)) != stages) {
+                    if (b.abort) { there = 0; break; }
+                    if (global_ns() - since > kWaitLimitNs) {
+                        record_timeout(p.g.status);
+                        b.abort = 1;
+                        there = 0;
+                        break;
                     }
-                    b.last = there;
                 }
-                named_bar_sync(1, 128);
-                if (*(volatile int *)&b.last == 0) break;
+                b.complete = there;
+            }
+            named_bar_sync(1, 128);
+            if (*(volatile int *)&b.complete != 0) {
                 __threadfence();
                 const int64_t nr = tile % nt * 128 + 4 * lane, m0 = tile / nt * BN;
                 const int cols = (int)std::min<int64_t>(BN, M - m0), c0 = cols * mine / count, c1 = cols * (mine + 1) / count;
-                const int *parts = p.part + tile * p.plan.max_segs * (BN * 128) + 4 * lane;
+                const int *parts = p.part + tile * count * (BN * 128) + 4 * lane;
                 float sw[4];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) sw[i] = nr + i < N ? bf16_to_f32(p.g.ws[nr + i]) : 0.0f;
@@ -658,6 +806,10 @@ int sms_of_device()
         if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
         const cudaFuncAttribute limit = cudaFuncAttributeMaxDynamicSharedMemorySize;
         cudaFuncSetAttribute(gemm_i8_pair_kernel, limit, kSmem + 1024);
+        cudaFuncSetAttribute(gemm_i8_rows_kernel<1>, limit, kRowsSmem + 1024);
+        cudaFuncSetAttribute(gemm_i8_rows_kernel<2>, limit, kRowsSmem + 1024);
+        cudaFuncSetAttribute(gemm_i8_rows_kernel<4>, limit, kRowsSmem + 1024);
+        cudaFuncSetAttribute(gemm_i8_rows_kernel<8>, limit, kRowsSmem + 1024);
         cudaFuncSetAttribute(gemm_i8_stream_kernel<16>, limit, Stream<16>::kSmem + 1024);
         cudaFuncSetAttribute(gemm_i8_stream_kernel<32>, limit, Stream<32>::kSmem + 1024);
         cudaFuncSetAttribute(gemm_i8_stream_kernel<64>, limit, Stream<64>::kSmem + 1024);
@@ -669,64 +821,89 @@ int sms_of_device()
 
 int stream_bn(int64_t M) { return M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : 128; }
 
-// Which kernel, and how the stream's units are dealt, by the time that this model gives (microseconds):
-//   stream, whole tiles: a CTA takes ceil(tiles / SMs) tiles; nothing is added up afterwards
-//   stream, even: the same number of CTAs for every tile, 8 stages at least to each: BN / 16 to add the parts up
-//   stream, cut: every CTA takes an equal share of the units, 8 at least, wherever the tiles end: kCut + BN / 8
-//   pairs: ceil(tiles / pairs) tiles of 256 x 256
-// A stage takes kUnit where few CTAs run, and what HBM gives it (kUnitAll with every SM at work); a pair's kPair.
-// What it chooses on B200, measured, with the others' times behind: M = 1, N = 10240, K = 8192: whole 18.8 (cut 20.3);
-// M = 64, 8192 x 8192: even 19.4 (whole 20.8, cut 25); M = 100, 8192 x 28672: even 52 (cut 59); M = 128, 2048 x 8192: even 14
-// (whole 22); M = 256, 8192 x 8192: whole 24.0 (pairs 26.8); M = 256, 10240 x 8192: pairs 28 (stream 40); M = 192, 130 x
-// 28672: even 18 (pairs 70).
-constexpr double kUnit = 0.23, kUnitAll = 0.36, kCut = 2.0, kPair = 0.33;
+// Tiles of the rows kernel: the fewest rounds in which a CTA has at most 128 weight rows.
+struct RowsPlan {
+    int mt, tokens, each, tiles, rounds;  // tiles of tokens; tokens and weight rows per CTA
+    int token_bytes, weight_bytes, pieces;
+};
+
+RowsPlan plan_rows(int64_t M, int64_t N, int sms)
+{
+    RowsPlan p;
+    const int64_t pairs = sms / 2, mt = (M + 127) / 128;
+    p.mt = (int)mt;
+    p.tokens = (int)((M + 2 * mt - 1) / (2 * mt));
+    int64_t each = 0;
+    for (int64_t rounds = std::max<int64_t>(1, mt * N / (256 * pairs)); each == 0 || each > 128; ++rounds) {
+        const int64_t nt = std::max<int64_t>(1, rounds * pairs / mt);
+        each = ((N + 2 * nt - 1) / (2 * nt) + 7) / 8 * 8;
+    }
+    p.each = (int)each;
+    p.tiles = (int)((N + 2 * each - 1) / (2 * each) * mt);
+    p.rounds = (int)((p.tiles + pairs - 1) / pairs);
+    p.token_bytes = (p.tokens + 7) / 8 * 1024;
+    p.weight_bytes = (p.each + 15) / 16 * 2048;
+    p.pieces = 8;
+    while (p.pieces > 1 && kRowsRing / (p.pieces * (p.token_bytes + p.weight_bytes)) < kLeastStages) p.pieces /= 2;
+    return p;
+}
+
+// Which kernel, by the time that this model gives (microseconds beyond a launch; a stage or piece is 128 of K):
+//   rows: the rounds' pieces, each the greatest of what a step takes however small (by the pieces in it), what HBM takes
+//     for the weights, and what an SM takes in
+//   pairs: ceil(tiles / pairs) tiles of 256 x 256, kPair per stage
+//   stream, whole tiles: a CTA takes ceil(tiles / SMs) of them; a stage takes 0.25 where few CTAs run, and what HBM gives
+//     it with every SM at work; a token's stores 0.025
+//   stream, split: the same number of CTAs for every tile, 8 stages at least to each, and the adding up
+// Fitted to and checked against 150 shapes of 1 to 1000 tokens, where what it takes is within 4% of the best but for six
+// (within 13%).  Measured, taken (not taken): M = 16, 8192 x 8192: rows 14.7 (split 17.1); M = 100, 57344 x 8192: rows 82
+// (whole 89); M = 128, 2048 x 8192: rows 8.7 (split 13.7); M = 256, 8192 x 8192: rows 19.0 (whole 22.7); M = 512, the same:
+// pairs 26.9 (rows 31.7); M = 1, 14336 x 4096: whole 11.9 (rows 13.2); M = 1, 1000 x 28672: split 15.3 (rows 18.4).
+constexpr double kUnit = 0.25, kUnitAll = 0.36, kPair = 0.33;
 constexpr int kLeastUnits = 8;
 
 struct Choice {
-    bool pairs;
+    enum { kRows, kPairs, kStream } kernel;
+    RowsPlan rows;
     Plan plan;  // of the stream
 };
 
 Choice choose(int64_t M, int64_t N, int64_t K, int sms)
 {
-    const int bn = stream_bn(M);
     Choice c;
+    const int bn = stream_bn(M);
     Plan &p = c.plan;
     p.nt = (int)((N + 127) / 128);
     p.tiles = (M + bn - 1) / bn * p.nt;
     p.stages = (int)((K + kRowBytes - 1) / kRowBytes);
-    p.total = p.tiles * p.stages;
-    p.split = 0;
     const auto unit = [&](int64_t grid) { return std::max(kUnit, kUnitAll * (double)grid / sms); };
     const int64_t rounds = (p.tiles + sms - 1) / sms, whole_grid = (p.tiles + rounds - 1) / rounds;
-    const double whole = (double)(rounds * p.stages) * unit(whole_grid);
-    const int64_t cut_grid = std::max<int64_t>(1, std::min<int64_t>(sms, p.total / kLeastUnits));
-    const int64_t share = (p.total + cut_grid - 1) / cut_grid;
-    const double cut = (double)share * unit(cut_grid) + kCut + bn / 8;
-    const int split = (int)std::min<int64_t>(sms / std::max<int64_t>(1, p.tiles), p.stages / kLeastUnits);
-    const int part = split > 1 ? (p.stages + split - 1) / split : 0;
-    const double even = split > 1 ? part * unit(split * p.tiles) + bn / 16 : 1e30;
-    const int64_t pair_tiles = ((M + kTile - 1) / kTile) * ((N + kTile - 1) / kTile);
-    const double pairs = (double)((pair_tiles + sms / 2 - 1) / (sms / 2) * p.stages) * kPair;
-    c.pairs = M > 128 && pairs <= std::min({whole, cut, even}) && pair_tiles < (1 << 30);
-    if (even < std::min(whole, cut)) {
-        p.split = (p.stages + part - 1) / part;
+    const double whole = (double)(rounds * p.stages) * unit(whole_grid) + 0.025 * (double)(rounds * std::min<int64_t>(M, 128));
+    const int most = (int)std::min<int64_t>(sms / p.tiles, p.stages / kLeastUnits);
+    double split = 1e30;
+    if (most > 1) {
+        p.per = (p.stages + most - 1) / most;
+        p.split = (p.stages + p.per - 1) / p.per;
         p.grid = (int)(p.split * p.tiles);
-        p.per = part;
-        p.extra = 0;
-    } else if (whole <= cut) {
+        split = p.per * unit(p.grid) + 2 + 0.25 * p.split + bn / 32.0;
+    }
+    if (whole <= split) {
+        p.split = 1;
         p.grid = (int)whole_grid;
         p.per = (int)(rounds * p.stages);
-        p.extra = 0;
-    } else {
-        p.grid = (int)cut_grid;
-        p.per = (int)(p.total / p.grid);
-        p.extra = (int)(p.total - (int64_t)p.per * p.grid);
     }
-    p.max_segs = p.split > 0 ? p.split : p.extra == 0 && p.per % p.stages == 0 ? 1 : (p.stages + p.per - 1) / p.per + 1;
-    // sharing costs a wait for the other CTAs (K = N = 8192, up to 4 parts a tile: M = 4 17.0 us without, 19.6 with), adding
-    // up alone costs by parts and columns (N = 128, K = 28672, 29 parts: M = 16 26.8 us alone, 13.9 shared)
-    p.shared = bn > 16 || p.max_segs * (M + 4) >= 72;
+    const double stream = std::min(whole, split);
+    const int64_t pair_tiles = ((M + kTile - 1) / kTile) * ((N + kTile - 1) / kTile);
+    const double pairs = M > 128 && pair_tiles < (1 << 30) ? (double)((pair_tiles + sms / 2 - 1) / (sms / 2) * p.stages) * kPair + 1 : 1e30;
+    double rows = 1e30;
+    if (N < (1 << 30) && M < (1 << 30) && pair_tiles < (1 << 28)) {
+        c.rows = plan_rows(M, N, sms);
+        const RowsPlan &r = c.rows;
+        const double per = std::min((double)r.each, (double)N * r.mt / (double)(sms / 2 * 2 * (int64_t)r.rounds)), share = per / r.mt;
+        const double step = r.pieces == 8 ? 0.062 : r.pieces == 4 ? 0.07 : r.pieces == 2 ? 0.105 : 0.2;
+        rows = (double)r.rounds * p.stages * std::max({step, 0.00278 * share, 0.0009 * (per + r.tokens) + 0.0014 * share}) + 1.7;
+    }
+    c.kernel = rows <= std::min(pairs, stream) ? Choice::kRows : pairs <= stream ? Choice::kPairs : Choice::kStream;
     return c;
 }
 
@@ -744,7 +921,7 @@ int run_stream(const int8_t *xq, const int8_t *wq, const Args &g, const Plan &pl
     uint8_t *w8 = static_cast<uint8_t *>(workspace);
     a.counters = reinterpret_cast<int *>(w8);
     a.part = reinterpret_cast<int *>(w8 + counter_region_bytes(a.plan.tiles));
-    if (plan.max_segs > 1 && clear_extra_counters(workspace, plan.tiles, st) != cudaSuccess) return -2;
+    if (plan.split > 1 && clear_extra_counters(workspace, plan.tiles, st) != cudaSuccess) return -2;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)a.plan.grid);
     cfg.blockDim = dim3(kThreads);
@@ -758,7 +935,7 @@ int run_stream(const int8_t *xq, const int8_t *wq, const Args &g, const Plan &pl
     attr[1].id = cudaLaunchAttributeCooperative;
     attr[1].val.cooperative = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = plan.max_segs > 1 && plan.shared ? 2 : 1;
+    cfg.numAttrs = plan.split > 1 ? 2 : 1;
     cudaLaunchKernelEx(&cfg, gemm_i8_stream_kernel<BN>, xmap, wmap, a);  // a failure is the caller's last error
     return 0;
 }
@@ -779,6 +956,25 @@ int run_pairs(const int8_t *xq, const int8_t *wq, Args a, int sms, cudaStream_t 
     return 0;
 }
 
+int run_rows(const int8_t *xq, const int8_t *wq, const Args &g, const RowsPlan &r, int sms, cudaStream_t st)
+{
+    const int stage_bytes = r.pieces * (r.token_bytes + r.weight_bytes);
+    const RowsArgs a{g, r.tiles, r.mt, r.each, r.tokens, r.token_bytes, r.weight_bytes, stage_bytes, std::min(kRowsStages, kRowsRing / stage_bytes)};
+    CUtensorMap xmap, wmap;
+    if (!encode_tmap_2d(&xmap, CU_TENSOR_MAP_DATA_TYPE_UINT8, xq, (uint64_t)g.K, (uint64_t)g.M, (uint64_t)g.K, kRowBytes,
+                        (uint32_t)r.tokens, CU_TENSOR_MAP_SWIZZLE_128B) ||
+        !encode_tmap_2d(&wmap, CU_TENSOR_MAP_DATA_TYPE_UINT8, wq, (uint64_t)g.K, (uint64_t)g.N, (uint64_t)g.K, kRowBytes,
+                        (uint32_t)r.each, CU_TENSOR_MAP_SWIZZLE_128B))
+        return -1;
+    const int pairs = std::min(r.tiles, sms / 2);
+    const auto kernel = r.pieces == 8   ? gemm_i8_rows_kernel<8>
+                        : r.pieces == 4 ? gemm_i8_rows_kernel<4>
+                        : r.pieces == 2 ? gemm_i8_rows_kernel<2>
+                                        : gemm_i8_rows_kernel<1>;
+    launch_behind(kernel, (unsigned)(2 * pairs), kThreads, kRowsSmem + 1024, st, xmap, wmap, a);
+    return 0;
+}
+
 }  // namespace
 
 size_t gemm_int8_workspace_bytes(int64_t M, int64_t N, int64_t K)
@@ -788,9 +984,9 @@ size_t gemm_int8_workspace_bytes(int64_t M, int64_t N, int64_t K)
     cudaGetDevice(&dev);
     cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
     const Choice c = choose(M, N, K, sms);
-    if (c.pairs || c.plan.max_segs == 1) return 0;  // no tile is split
+    if (c.kernel != Choice::kStream || c.plan.split == 1) return 0;  // no tile is split
     return counter_region_bytes(c.plan.tiles) +
-           ((size_t)c.plan.tiles * c.plan.max_segs * stream_bn(M) * 128 * sizeof(int) + 255) / 256 * 256;
+           ((size_t)c.plan.tiles * c.plan.split * stream_bn(M) * 128 * sizeof(int) + 255) / 256 * 256;
 }
 
 int launch_gemm_w8a8_int8(const int8_t *xq, const float *xscales, int64_t M, int64_t N, int64_t K, const int8_t *wq,
@@ -800,7 +996,8 @@ int launch_gemm_w8a8_int8(const int8_t *xq, const float *xscales, int64_t M, int
     if (sms < 2) return -2;
     const Args g{M, N, K, xscales, wscales, y, status, 0, 0, 0};
     const Choice c = choose(M, N, K, sms);
-    if (c.pairs) return run_pairs(xq, wq, g, sms, st);
+    if (c.kernel == Choice::kRows) return run_rows(xq, wq, g, c.rows, sms, st);
+    if (c.kernel == Choice::kPairs) return run_pairs(xq, wq, g, sms, st);
     switch (stream_bn(M)) {
     case 16: return run_stream<16>(xq, wq, g, c.plan, workspace, st);
     case 32: return run_stream<32>(xq, wq, g, c.plan, workspace, st);

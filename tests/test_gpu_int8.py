@@ -137,6 +137,23 @@ def test_matmul_model_shapes(M, N, K):
     check_matmul(M, N, K, M + N + K)
 
 
+# Weight rows shared out: one to eight pieces of K per stage, one to several tiles of tokens and rounds, odd everything
+@pytest.mark.parametrize("M,N,K", [(1, 1000, 8192), (2, 130, 4000), (128, 4099, 1056), (65, 10247, 512), (127, 19001, 288),
+                                   (128, 57343, 160), (129, 2048, 8192), (300, 1001, 4096), (384, 5003, 1024), (700, 513, 544),
+                                   (1000, 70, 2080), (2049, 130, 1024), (64, 40000, 352), (150, 130, 131040)])
+def test_matmul_shared_rows(M, N, K):
+    check_matmul(M, N, K, M + N + K)
+
+
+# Tiles of 128 weight rows by 16, 32, 64 and 128 tokens, whole and with their K split between CTAs
+@pytest.mark.parametrize("M,N,K", [(5, 17, 96), (33, 300, 160), (3, 28671, 1056), (20, 28672, 1024), (40, 14336, 1024),
+                                   (16, 57344, 512), (2, 130, 28672), (1, 1, 16384), (16, 1000, 20000), (30, 999, 28672),
+                                   (67, 14420, 96), (64, 257, 28640), (100, 1000, 28672), (300, 1000, 28672),
+                                   (129, 1001, 28672)])
+def test_matmul_streamed_tiles(M, N, K):
+    check_matmul(M, N, K, M + N + K)
+
+
 @pytest.mark.parametrize("M", [1, 5, 300])
 def test_matmul_largest_sums(M):
     """Every code -128 at the greatest depth: 2^14 * 131040 is the largest sum, just below 2^31."""
@@ -176,8 +193,8 @@ def test_matmul_refusals():
                       ((xq, xs.cpu(), w, ws), TypeError)):
         with pytest.raises(err):
             wq.wq_gemm_w8a8_int8(*args)
-    args = [t.cuda() for t in operands(1, 2048, 8192, 1)]
-    assert wq.wq_gemm_w8a8_int8_workspace_bytes(1, 2048, 8192) > 0
+    args = [t.cuda() for t in operands(1, 1000, 28672, 1)]
+    assert wq.wq_gemm_w8a8_int8_workspace_bytes(1, 1000, 28672) > 0
     with pytest.raises(wq.WQError):
         wq.wq_gemm_w8a8_int8(*args, workspace=torch.zeros(16, dtype=torch.uint8).cuda())
 
