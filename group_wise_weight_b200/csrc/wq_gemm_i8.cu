@@ -14,16 +14,16 @@
 // Few and middling rows (gemm_i8_rows_kernel): the weights bound the call, so
 // their rows are shared out evenly, rounded up to 8: up to 128 tokens N / 148 of
 // them to an SM (in rounds of at most 128), beyond that tiles of up to 128
-// tokens, the ones on the same weights next to one another; no sum is split.  A pair of CTAs
-// computes 128 tokens by twice that many weight rows: each loads its weight
-// rows and half of the tokens, which halves what the tokens take of an SM's
-// intake, and the pair's MMA (128 x up to 256) reads both halves.  Stages hold
-// several pieces of 128 bytes of K, as many as leave 5 stages in the ring: a
-// weight row's bytes then come in runs of up to 1 KB, which DRAM gives faster
-// (M = 1, 8192 x 28672: pieces singly 52.3 us, two 39.5, four 38.6; N = 1000:
-// 50.2, 32, 21).  Measured: M = 1, 10240 x 8192 17.4 us (4.8 TB/s); 8192 x 28672
-// 38.9 (6.0); M = 100, the same 43.3 us; M = 384, 2048 x 8192 11.5 us.  With the
-// other two kernels: 18.9, 39.8, 51.6, 20.9.
+// tokens, the ones on the same weights next to one another; no sum is split.
+// A pair of CTAs computes 128 tokens by twice that many weight rows: each loads
+// its weight rows and half of the tokens, which halves what the tokens take of
+// an SM's intake, and the pair's MMA (128 x up to 256) reads both halves.
+// Stages hold several pieces of 128 bytes of K, as many as leave 5 stages in
+// the ring: a weight row's bytes then come in runs of up to 1 KB, which DRAM
+// gives faster (M = 1, 8192 x 28672: pieces singly 52.3 us, two 39.5, four
+// 38.6; N = 1000: 50.2, 32, 21).  Measured: M = 1, 10240 x 8192 17.5 us (4.8
+// TB/s), 8192 x 28672 38.3 (6.1 TB/s); M = 100, the same 42.6 us; M = 384, 2048
+// x 8192 11.7 us.  With the other two kernels: 18.9, 39.8, 51.5, 20.9.
 //
 // Few weight rows and a deep K, or few rows and a shallow one
 // (gemm_i8_stream_kernel): tiles of 128 weight rows (the MMA's M, so a token

@@ -23,7 +23,7 @@
 // longer one to a CTA of 256 or 512 threads, 8 values per thread and chunk;
 // rows beyond 32,768 values are read twice (the second time from L2).
 // Measured: 8,192 x 28,672 bf16 115 us (6.1 TB/s, 93% of a copy); one row of
-// 8,192 6.3 us, which is what the host needs to make the calls.
+// 8,192 4.7 us, which is what the host needs to make the calls (1.9 in a graph).
 #include "wq_internal.h"
 #include "wq_prompt.cuh"
 #include "wq_quotient.cuh"

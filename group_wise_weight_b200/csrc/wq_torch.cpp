@@ -3,7 +3,7 @@
 // A call of these operators at decode sizes is a few microseconds of kernel,
 // so what the host does around the launch is what a user waits for: the same
 // checks, output allocations and ctypes marshalling in Python took 11 to 16
-// microseconds a call, this file's 3 to 7 (B200 host, calls back to back).
+// microseconds a call, this file's 3 to 5.5 (B200 host, calls back to back).
 // It marshals arguments only: types, shapes, strides and devices are checked
 // here, everything else by the C entry points of libwq (include/wq.h), whose
 // status codes go back through the `raise_status` callable.
