@@ -45,7 +45,9 @@
 // gives every SM at once.  A pair of CTAs computes 256 x 256: each holds the
 // accumulators of its 128 rows of activations and loads those and half of the
 // tile's 256 weight rows; the pair's MMA reads both halves, so an SM takes in
-// 64 bytes per cycle.  Warp 0 of each CTA copies, its completions counted by
+// 64 bytes per cycle.  The tile's weight rows are fewer, in steps of 32, where
+// that fills the last round (M = 700, 8192 x 8192: 45.3 -> 38.9 us; M = 256,
+// 10240 x 8192: 27.9 -> 24.3).  Warp 0 of each CTA copies, its completions counted by
 // the leader CTA's barrier; in the leader, one thread of warp 1 issues the
 // pair's MMAs and their commits, which reach both CTAs; warps 2-5 turn one of
 // two accumulators into bf16 while the MMAs fill the other.  Tiles are taken
@@ -90,7 +92,7 @@ struct Args {
     const uint16_t *ws;
     uint16_t *y;
     int *status;
-    int mt, nt, band;  // tiles of rows and columns, row tiles per band
+    int mt, nt, band, each;  // tiles of rows and columns, row tiles per band, weight rows per CTA and tile (a multiple of 16)
 };
 
 __device__ __forceinline__ uint32_t cluster_rank()
@@ -241,11 +243,11 @@ gemm_i8_pair_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_const
             for (int t = pair; ok && t < tiles; t += pairs) {
                 int mi, ni;
                 tile_at(p, t, mi, ni);
-                const int m = mi * kTile + (int)rank * kHalf, n = ni * kTile + (int)rank * kHalf;
+                const int m = mi * kTile + (int)rank * kHalf, n = (2 * ni + (int)rank) * p.each;
                 for (int s = 0; s < stages; ++s) {
                     if (issued >= (uint32_t)kStages && !wait(&b.empty[slot], phase ^ 1u)) { ok = false; break; }
                     uint8_t *st = smem + slot * kStageBytes;
-                    if (rank == 0) mbar_arrive_expect_tx(&b.full[slot], 2 * kStageBytes);  // both CTAs' bytes
+                    if (rank == 0) mbar_arrive_expect_tx(&b.full[slot], 2 * (kOperand + p.each * kRowBytes));  // both CTAs' bytes
                     const uint32_t bar = at_leader(&b.full[slot]);
                     load_pair(st, &xmap, bar, s * kRowBytes, m);
                     load_pair(st + kOperand, &wmap, bar, s * kRowBytes, n);
@@ -268,7 +270,7 @@ gemm_i8_pair_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_const
         if (rank == 0 && elect_one()) {
             uint32_t slot = 0, phase = 0, n = 0;
             const uint32_t base = smem_u32(smem);
-            constexpr uint32_t idesc = idesc_s8_s32(kTile, kTile);
+            const uint32_t idesc = idesc_s8_s32(kTile, 2 * p.each);
             bool ok = true;
             for (int t = pair; ok && t < tiles; t += pairs, ++n) {
                 const uint32_t buf = n & 1u;
@@ -305,18 +307,17 @@ gemm_i8_pair_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_const
         for (int t = pair; t < tiles; t += pairs, ++n) {
             int mi, ni;
             tile_at(p, t, mi, ni);
-            const int64_t m0 = (int64_t)mi * kTile + rank * kHalf + quarter * 32, n0 = (int64_t)ni * kTile;
+            const int64_t m0 = (int64_t)mi * kTile + rank * kHalf + quarter * 32, n0 = (int64_t)ni * 2 * p.each;
             named_bar_sync(1, 128);  // the scales of the tile before have been read
-            for (int i = et; i < kTile; i += 128) sw[i] = n0 + i < p.N ? bf16_to_f32(p.ws[n0 + i]) : 0.0f;
+            for (int i = et; i < 2 * p.each; i += 128) sw[i] = n0 + i < p.N ? bf16_to_f32(p.ws[n0 + i]) : 0.0f;
             named_bar_sync(1, 128);
             const float sx = m0 + lane < p.M ? p.xs[m0 + lane] : 0.0f;
             const uint32_t buf = n & 1u;
             if (!wait(&b.d_full[buf], (n >> 1) & 1u)) break;
             tc_fence_after();
-            const int rows = (int)min((int64_t)32, p.M - m0), cols = (int)min((int64_t)kTile, p.N - n0);
+            const int rows = (int)min((int64_t)32, p.M - m0), cols = (int)min((int64_t)2 * p.each, p.N - n0);
 #pragma unroll 1
-            for (int c = 0; c < kTile; c += 32) {
-                if (c >= cols || rows <= 0) break;
+            for (int c = 0; c < cols && rows > 0; c += 32) {
                 uint32_t v[32];
                 tmem_ld32(tmem + lane_bits + buf * 256u + (uint32_t)c, v);
                 tmem_wait_ld();
@@ -848,15 +849,36 @@ RowsPlan plan_rows(int64_t M, int64_t N, int sms)
     return p;
 }
 
+// Tiles of the pair kernel: 256 tokens by the weight rows that fill the fewest rounds evenly.
+struct PairPlan {
+    int mt, nt, each, rounds;  // tiles of tokens and of weight rows; weight rows per CTA
+};
+
+PairPlan plan_pairs(int64_t M, int64_t N, int sms)
+{
+    PairPlan p;
+    const int64_t pairs = sms / 2, mt = (M + kTile - 1) / kTile;
+    int64_t each = 0;
+    for (int64_t rounds = std::max<int64_t>(1, mt * N / (kTile * pairs)); each == 0 || each > kHalf; ++rounds) {
+        const int64_t nt = std::max<int64_t>(1, rounds * pairs / mt);
+        each = ((N + 2 * nt - 1) / (2 * nt) + 15) / 16 * 16;
+    }
+    p.mt = (int)mt;
+    p.each = (int)each;
+    p.nt = (int)((N + 2 * each - 1) / (2 * each));
+    p.rounds = (int)((mt * p.nt + pairs - 1) / pairs);
+    return p;
+}
+
 // Which kernel, by the time that this model gives (microseconds beyond a launch; a stage or piece is 128 of K):
 //   rows: the rounds' pieces, each the greatest of what a step takes however small (by the pieces in it), what HBM takes
 //     for the weights, and what an SM takes in
-//   pairs: ceil(tiles / pairs) tiles of 256 x 256, kPair per stage
+//   pairs: the rounds' stages, each kPair in proportion to the tile's weight rows, or what HBM or an SM takes as above
 //   stream, whole tiles: a CTA takes ceil(tiles / SMs) of them; a stage takes 0.25 where few CTAs run, and what HBM gives
 //     it with every SM at work; a token's stores 0.025
 //   stream, split: the same number of CTAs for every tile, 8 stages at least to each, and the adding up
-// Fitted to and checked against 150 shapes of 1 to 1000 tokens, where what it takes is within 4% of the best but for six
-// (within 13%).  Measured, taken (not taken): M = 16, 8192 x 8192: rows 14.7 (split 17.1); M = 100, 57344 x 8192: rows 82
+// Fitted to and checked against 250 shapes of 1 to 2000 tokens, where what it takes is within 5% of the best but for
+// 17 (within 14%).  Measured, taken (not taken): M = 16, 8192 x 8192: rows 14.7 (split 17.1); M = 100, 57344 x 8192: rows 82
 // (whole 89); M = 128, 2048 x 8192: rows 8.7 (split 13.7); M = 256, 8192 x 8192: rows 19.0 (whole 22.7); M = 512, the same:
 // pairs 26.9 (rows 31.7); M = 1, 14336 x 4096: whole 11.9 (rows 13.2); M = 1, 1000 x 28672: split 15.3 (rows 18.4).
 constexpr double kUnit = 0.25, kUnitAll = 0.36, kPair = 0.33;
@@ -865,6 +887,7 @@ constexpr int kLeastUnits = 8;
 struct Choice {
     enum { kRows, kPairs, kStream } kernel;
     RowsPlan rows;
+    PairPlan pairs;
     Plan plan;  // of the stream
 };
 
@@ -894,7 +917,12 @@ Choice choose(int64_t M, int64_t N, int64_t K, int sms)
     }
     const double stream = std::min(whole, split);
     const int64_t pair_tiles = ((M + kTile - 1) / kTile) * ((N + kTile - 1) / kTile);
-    const double pairs = M > 128 && pair_tiles < (1 << 30) ? (double)((pair_tiles + sms / 2 - 1) / (sms / 2) * p.stages) * kPair + 1 : 1e30;
+    double pairs = 1e30;
+    if (M > 128 && pair_tiles < (1 << 30)) {
+        c.pairs = plan_pairs(M, N, sms);
+        const double each = c.pairs.each, share = each / c.pairs.mt;
+        pairs = (double)c.pairs.rounds * p.stages * std::max({kPair * each / kHalf, 0.00278 * share, 0.0009 * (each + kHalf) + 0.0014 * share}) + 1;
+    }
     double rows = 1e30;
     if (N < (1 << 30) && M < (1 << 30) && pair_tiles < (1 << 28)) {
         c.rows = plan_rows(M, N, sms);
@@ -940,16 +968,17 @@ int run_stream(const int8_t *xq, const int8_t *wq, const Args &g, const Plan &pl
     return 0;
 }
 
-int run_pairs(const int8_t *xq, const int8_t *wq, Args a, int sms, cudaStream_t st)
+int run_pairs(const int8_t *xq, const int8_t *wq, Args a, const PairPlan &r, int sms, cudaStream_t st)
 {
     CUtensorMap xmap, wmap;
     if (!encode_tmap_2d(&xmap, CU_TENSOR_MAP_DATA_TYPE_UINT8, xq, (uint64_t)a.K, (uint64_t)a.M, (uint64_t)a.K, kRowBytes, kHalf,
                         CU_TENSOR_MAP_SWIZZLE_128B) ||
-        !encode_tmap_2d(&wmap, CU_TENSOR_MAP_DATA_TYPE_UINT8, wq, (uint64_t)a.K, (uint64_t)a.N, (uint64_t)a.K, kRowBytes, kHalf,
+        !encode_tmap_2d(&wmap, CU_TENSOR_MAP_DATA_TYPE_UINT8, wq, (uint64_t)a.K, (uint64_t)a.N, (uint64_t)a.K, kRowBytes, (uint32_t)r.each,
                         CU_TENSOR_MAP_SWIZZLE_128B))
         return -1;
-    a.mt = (int)((a.M + kTile - 1) / kTile);
-    a.nt = (int)((a.N + kTile - 1) / kTile);
+    a.mt = r.mt;
+    a.nt = r.nt;
+    a.each = r.each;
     a.band = (int)std::max<int64_t>(1, std::min<int64_t>(a.mt, kBandBytes / (kTile * a.K)));
     const int64_t pairs = std::min<int64_t>((int64_t)a.mt * a.nt, sms / 2);
     launch_behind(gemm_i8_pair_kernel, (unsigned)(2 * pairs), kThreads, kSmem + 1024, st, xmap, wmap, a);
@@ -994,10 +1023,10 @@ int launch_gemm_w8a8_int8(const int8_t *xq, const float *xscales, int64_t M, int
 {
     const int sms = sms_of_device();
     if (sms < 2) return -2;
-    const Args g{M, N, K, xscales, wscales, y, status, 0, 0, 0};
+    const Args g{M, N, K, xscales, wscales, y, status, 0, 0, 0, 0};
     const Choice c = choose(M, N, K, sms);
     if (c.kernel == Choice::kRows) return run_rows(xq, wq, g, c.rows, sms, st);
-    if (c.kernel == Choice::kPairs) return run_pairs(xq, wq, g, sms, st);
+    if (c.kernel == Choice::kPairs) return run_pairs(xq, wq, g, c.pairs, sms, st);
     switch (stream_bn(M)) {
     case 16: return run_stream<16>(xq, wq, g, c.plan, workspace, st);
     case 32: return run_stream<32>(xq, wq, g, c.plan, workspace, st);

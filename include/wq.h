@@ -520,8 +520,8 @@ size_t wq_gemm_w8a8_int8_workspace_bytes(int64_t M, int64_t N, int64_t K);
  * wq_gemm_w8a8_int8_workspace_bytes bytes (may be NULL when that is 0), not
  * overlapping y; y must not overlap an input.
  * Kernels, chosen by a model of their times: one that shares the weights' rows
- * out evenly over pairs of SMs, one that computes 256 x 256 tiles on pairs, and
- * one that streams tiles of 128 weight rows, a tile's K split between CTAs where
+ * out evenly over pairs of SMs, one that computes tiles of 256 tokens by up to
+ * 256 weight rows on pairs, and one that streams tiles of 128 weight rows, a tile's K split between CTAs where
  * the weights have few rows and much K; only that needs workspace.  All run at
  * most one CTA per SM; where CTAs wait for one another's sums the launch is a
  * cooperative one, so that calls on several streams never hold the SMs that

@@ -145,6 +145,13 @@ def test_matmul_shared_rows(M, N, K):
     check_matmul(M, N, K, M + N + K)
 
 
+# Tiles of 256 tokens by 160 to 256 weight rows on pairs of SMs, one to several rounds of them
+@pytest.mark.parametrize("M,N,K", [(700, 8191, 1056), (300, 57345, 160), (256, 10243, 512), (1500, 4099, 2080), (513, 14337, 288),
+                                   (2000, 20011, 96), (150, 40001, 1024), (129, 57344, 544), (4097, 1001, 2048)])
+def test_matmul_pair_tiles(M, N, K):
+    check_matmul(M, N, K, M + N + K)
+
+
 # Tiles of 128 weight rows by 16, 32, 64 and 128 tokens, whole and with their K split between CTAs
 @pytest.mark.parametrize("M,N,K", [(5, 17, 96), (33, 300, 160), (3, 28671, 1056), (20, 28672, 1024), (40, 14336, 1024),
                                    (16, 57344, 512), (2, 130, 28672), (1, 1, 16384), (16, 1000, 20000), (30, 999, 28672),
