@@ -19,8 +19,8 @@
 //
 // The r = Hq / H query heads of a KV head share its keys and values: a tile's
 // 128 rows are (token, head) pairs, token-major, so it covers 128 / r tokens
-// and short sequences still fill it.  A work item is two such tiles
-// (consecutive tokens) of one KV head.  The grid has a CTA per item; one that
+// and short sequences still fill it.  A work item is two such tiles of one KV
+// head (consecutive tokens), or one.  The grid has a CTA per item; one that
 // runs claims further ones before they are launched (cluster launch control)
 // and does their items too, so an SM keeps its pipeline filled across items of
 // any length.
@@ -92,21 +92,21 @@ struct Cfg {
 struct PromptArgs {
     const int32_t *starts;
     int64_t M, ldo;
-    int B, H, r, tpt;  // tokens per tile
+    int B, H, r, tpt, tiles;  // tokens per tile, tiles per item
     float scale_log2;  // log2(e) / sqrt(D)
     uint16_t *o;
     int *status;
 };
 
-// One work item: tiles at tokens tok0 and tok0 + tpt of the sequence at row0, KV head h.
+// One work item: the tiles at tokens tok0 and, before `end`, tok0 + tpt of the sequence at row0, KV head h.
 struct Item {
     int64_t row0;
-    int len, tok0, h, valid;
+    int len, tok0, end, h, valid;
     // keys seen by some row of tile x, and its blocks (0: no such tile)
     __device__ __forceinline__ int last(int x, int tpt) const { return std::min(len, tok0 + (x + 1) * tpt); }
     __device__ __forceinline__ int blocks(int x, int tpt) const
     {
-        return tok0 + x * tpt < len ? (last(x, tpt) + kKeys - 1) / kKeys : 0;
+        return tok0 + x * tpt < end ? (last(x, tpt) + kKeys - 1) / kKeys : 0;
     }
     // block j holds the sequence's end within a step of 16 keys: its first row past the end, or 0
     __device__ __forceinline__ int tail(int j) const
@@ -139,7 +139,7 @@ struct Finder {
 
     __device__ __forceinline__ bool find(const PromptArgs &p, int64_t t, Item &it)
     {
-        const int lane = threadIdx.x & 31, span = 2 * p.tpt;
+        const int lane = threadIdx.x & 31, span = p.tiles * p.tpt;
         if (t < before) *this = Finder();
         for (;;) {
             if (t < before + all) break;
@@ -169,6 +169,7 @@ struct Finder {
         it.row0 = __shfl_sync(0xffffffffu, s, src);
         it.len = (int)__shfl_sync(0xffffffffu, e - s, src);
         it.tok0 = l * span;
+        it.end = std::min(it.len, it.tok0 + span);
         return true;
     }
 };
@@ -729,25 +730,30 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_consta
     if (wid == kMmaWarp) tmem_dealloc(tmem, kTmemCols);
 }
 
-// Raises the kernels' shared-memory limit on their first use on the current device.
-bool prepare_device()
+// SMs of the current device, 0 on failure; the kernels' shared-memory limits are raised on their first use there.
+int sms_of_device()
 {
-    static std::atomic<bool> ready[128] = {};
+    static std::atomic<int> sms_of[128] = {};
     int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 128) return false;
-    if (!ready[dev].load(std::memory_order_acquire)) {
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 128) return 0;
+    int sms = sms_of[dev].load(std::memory_order_acquire);
+    if (sms == 0) {
         const cudaFuncAttribute limit = cudaFuncAttributeMaxDynamicSharedMemorySize;
-        if (cudaFuncSetAttribute(prompt_attn_kernel<64>, limit, Cfg<64>::kBytes + 1024) != cudaSuccess ||
+        if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
+            cudaFuncSetAttribute(prompt_attn_kernel<64>, limit, Cfg<64>::kBytes + 1024) != cudaSuccess ||
             cudaFuncSetAttribute(prompt_attn_kernel<128>, limit, Cfg<128>::kBytes + 1024) != cudaSuccess)
-            return false;
-        ready[dev].store(true, std::memory_order_release);
+            return 0;
+        sms_of[dev].store(sms, std::memory_order_release);
     }
-    return true;
+    return sms;
 }
 
+// Items of at most `tiles` tiles: at most ceil(len / span) of a sequence and KV head.
+int64_t items(int64_t M, int64_t B, int64_t tpt, int64_t H, int tiles) { return (M / (tiles * tpt) + B) * H; }
+
 template <int D>
-int run(const uint16_t *q, int64_t ldq, const uint16_t *k, int64_t ldk, const uint16_t *v, int64_t ldv, int64_t Hq,
-        const PromptArgs &a, cudaStream_t st)
+int run(const uint16_t *q, int64_t ldq, const uint16_t *k, int64_t ldk, const uint16_t *v, int64_t ldv, int64_t Hq, PromptArgs a,
+        cudaStream_t st)
 {
     CUtensorMap qm, km, vm;
     const auto encode = [&](CUtensorMap *map, const uint16_t *base, int64_t heads, int64_t ld, int box_heads, int box_tokens) {
@@ -756,8 +762,12 @@ int run(const uint16_t *q, int64_t ldq, const uint16_t *k, int64_t ldk, const ui
     };
     if (!encode(&qm, q, Hq, ldq, a.r, a.tpt) || !encode(&km, k, a.H, ldk, 1, kKeys) || !encode(&vm, v, a.H, ldv, 1, kKeys))
         return -1;
-    if (!prepare_device()) return -2;
-    const unsigned grid = (unsigned)prompt_attention_items(a.M, a.B, a.r * (int64_t)a.H, a.H);
+    const int sms = sms_of_device();
+    if (sms == 0) return -2;
+    // Two tiles share a CTA's K and V and fill each other's waits; one to a CTA while that leaves SMs over (2,000 tokens, 4
+    // heads of 64: 23.0 us with one, 30.8 with two; 1,000 tokens, 16 / 2 heads of 128: 18.2 and 19.8)
+    a.tiles = (a.M / a.tpt + a.B / 2) * a.H <= sms ? 1 : 2;
+    const unsigned grid = (unsigned)items(a.M, a.B, a.tpt, a.H, a.tiles);
     launch_behind(prompt_attn_kernel<D>, grid, kThreads, Cfg<D>::kBytes + 1024, st, qm, km, vm, a);
     return 0;
 }
@@ -766,8 +776,7 @@ int run(const uint16_t *q, int64_t ldq, const uint16_t *k, int64_t ldk, const ui
 
 int64_t prompt_attention_items(int64_t M, int64_t B, int64_t Hq, int64_t H)
 {
-    const int64_t span = 2 * (kRows / (Hq / H));  // tokens of a pair of tiles: at most ceil(len / span) pairs per sequence
-    return (M / span + B) * H;
+    return items(M, B, kRows / (Hq / H), H, 1);
 }
 
 int launch_prompt_attention(const uint16_t *q, int64_t ldq, const uint16_t *k, int64_t ldk, const uint16_t *v,
@@ -775,7 +784,7 @@ int launch_prompt_attention(const uint16_t *q, int64_t ldq, const uint16_t *k, i
                             uint16_t *o, int64_t ldo, int *status, cudaStream_t st)
 {
     const int r = (int)(Hq / H);
-    const PromptArgs a{starts, M, ldo, (int)B, (int)H, r, kRows / r, 1.4426950408889634f / sqrtf((float)D), o, status};
+    const PromptArgs a{starts, M, ldo, (int)B, (int)H, r, kRows / r, 2, 1.4426950408889634f / sqrtf((float)D), o, status};
     return D == 128 ? run<128>(q, ldq, k, ldk, v, ldv, Hq, a, st) : run<64>(q, ldq, k, ldk, v, ldv, Hq, a, st);
 }
 

@@ -19,11 +19,13 @@
 //
 // The pass reads 2 or 4 bytes and writes 1 per value, so it is bound by HBM:
 // the row crosses it once, kept in registers between the maximum and the
-// codes.  A row of up to 2,048 values belongs to one warp (no barrier), a
-// longer one to a CTA of 256 or 512 threads, 8 values per thread and chunk;
-// rows beyond 32,768 values are read twice (the second time from L2).
+// codes.  A row of up to 2,048 values (1,024 in binary32) belongs to one warp
+// (no barrier), a longer one to a CTA of 256 or 512 threads, 8 values per thread
+// and chunk; rows beyond 32,768 values (8,192) are read twice (the second time
+// from L2).
 // Measured: 8,192 x 28,672 bf16 115 us (6.1 TB/s, 93% of a copy); one row of
-// 8,192 4.7 us, which is what the host needs to make the calls (1.9 in a graph).
+// 8,192 4.7 us, which is what the host needs to make the calls (1.9 in a graph);
+// binary32 4,096 x 8,192 32.6 us (5.1 TB/s), 4,096 x 14,336 68.5 us (4.3 TB/s).
 #include "wq_internal.h"
 #include "wq_prompt.cuh"
 #include "wq_quotient.cuh"
@@ -228,14 +230,23 @@ template <typename T>
 void dispatch(const T *x, int64_t M, int64_t K, int64_t ldx, int8_t *q, float *s, cudaStream_t st)
 {
     const unsigned rows = (unsigned)M, warps = (unsigned)((M + kWarpRows - 1) / kWarpRows);
-    if (K <= 512) launch_behind(quant_tokens_warp_kernel<T, 2>, warps, kWarpRows * 32, 0, st, x, M, K, ldx, q, s);
-    else if (K <= 1024) launch_behind(quant_tokens_warp_kernel<T, 4>, warps, kWarpRows * 32, 0, st, x, M, K, ldx, q, s);
-    else if (K <= 2048) launch_behind(quant_tokens_warp_kernel<T, 8>, warps, kWarpRows * 32, 0, st, x, M, K, ldx, q, s);
-    else if (K <= 4096) launch_behind(quant_tokens_row_kernel<T, 256, 2>, rows, 256, 0, st, x, K, ldx, q, s);
-    else if (K <= 8192) launch_behind(quant_tokens_row_kernel<T, 256, 4>, rows, 256, 0, st, x, K, ldx, q, s);
-    else if (K <= 16384) launch_behind(quant_tokens_row_kernel<T, 512, 4>, rows, 512, 0, st, x, K, ldx, q, s);
-    else if (K <= 32768) launch_behind(quant_tokens_row_kernel<T, 512, 8>, rows, 512, 0, st, x, K, ldx, q, s);
-    else launch_behind(quant_tokens_long_kernel<T, 512>, rows, 512, 0, st, x, K, ldx, q, s);
+    const auto per_warp = [&](auto kernel) { launch_behind(kernel, warps, kWarpRows * 32, 0, st, x, M, K, ldx, q, s); };
+    const auto per_cta = [&](auto kernel, unsigned threads) { launch_behind(kernel, rows, threads, 0, st, x, K, ldx, q, s); };
+    if (K <= 512) per_warp(quant_tokens_warp_kernel<T, 2>);
+    else if (K <= 1024) per_warp(quant_tokens_warp_kernel<T, 4>);
+    else if (sizeof(T) == 4) {
+        // binary32: at most 16 values in a thread's registers, so that the SM holds enough rows (32 values: 8,192 x 2,048 30.5
+        // us, 4,096 x 8,192 36.4, 4,096 x 14,336 80.0); beyond 8,192 the second read costs less than one row per SM
+        if (K <= 2048) per_cta(quant_tokens_row_kernel<T, 256, 1>, 256);
+        else if (K <= 4096) per_cta(quant_tokens_row_kernel<T, 256, 2>, 256);
+        else if (K <= 8192) per_cta(quant_tokens_row_kernel<T, 512, 2>, 512);
+        else per_cta(quant_tokens_long_kernel<T, 1024>, 1024);
+    } else if (K <= 2048) per_warp(quant_tokens_warp_kernel<T, 8>);
+    else if (K <= 4096) per_cta(quant_tokens_row_kernel<T, 256, 2>, 256);
+    else if (K <= 8192) per_cta(quant_tokens_row_kernel<T, 256, 4>, 256);
+    else if (K <= 16384) per_cta(quant_tokens_row_kernel<T, 512, 4>, 512);
+    else if (K <= 32768) per_cta(quant_tokens_row_kernel<T, 512, 8>, 512);
+    else per_cta(quant_tokens_long_kernel<T, 512>, 512);
 }
 
 }  // namespace

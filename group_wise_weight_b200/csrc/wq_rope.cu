@@ -27,7 +27,7 @@
 // sines and cosines are formed, and the kernel starts while the previous one
 // ends (without the two 128 tokens took 7.3 us, 16,384 104).
 // Measured: 16,384 tokens, 64 + 8 heads of 128 with norms, 100 us (6.0 TB/s,
-// 92% of a copy); 128 tokens 5.7 us, 4.4 in a graph: launch and load latency.
+// 92% of a copy); 128 tokens 5.0 us, 3.7 in a graph: launch and load latency.
 #include <algorithm>
 
 #include "wq_internal.h"
@@ -170,8 +170,10 @@ __device__ __forceinline__ void turn_heads(Batch &first, const uint16_t *src, ui
     }
 }
 
+// 64 registers, so that an SM holds 32 warps (with 74 and 24 of them: 128 tokens of 72 heads 4.4 us, now 3.7; 8,192 of 40 heads
+// of 64 17.9, 16.4; 16,384 of 72 100.5, 101.5).
 template <int D, bool INTERLEAVED, bool NORM>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, 4)
 qk_norm_rope_kernel(const RopeArgs p)
 {
     constexpr int L = D / 8, kHeads = 32 / L;  // heads per warp at a time

@@ -606,7 +606,7 @@ int wq_kv_store_fp8(const uint16_t *k, int64_t ldk, const uint16_t *v, int64_t l
  * Requirements: B, M >= 1; D 64 or 128, Hq % H == 0, Hq / H <= 64
  * (WQ_ERR_UNSUPPORTED otherwise); row distances >= heads * D and multiples of
  * 8; q, k, v, o 16-byte aligned, starts 4-byte; M <= 2^25, B <= 2^20, Hq <=
- * 65535 and, with T = 128 H / Hq rounded down, (M / (2 T) + B) * H below 2^31
+ * 65535 and, with T = 128 H / Hq rounded down, (M / T + B) * H below 2^31
  * (WQ_ERR_SHAPE); o must not overlap an input (columns of one buffer, with the same row
  * distance, are apart).  `starts` that break the rule above are clamped: what
  * they ask for is unspecified, but nothing outside the M rows is touched.

@@ -89,6 +89,13 @@ def test_groups(Hq, H, D):
 
 
 @pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("n", [1, 127, 128, 129, 255, 256, 257, 385, 513, 700])
+def test_two_tiles_to_an_item(n, D):
+    """More work than SMs: a CTA takes two tiles at a time, the second of them absent, cut short or whole."""
+    run([n, 0, 300], 64, 64, D, n)
+
+
+@pytest.mark.parametrize("D", [64, 128])
 def test_ragged_pack_with_empty_sequences(D):
     run([0, 5, 0, 0, 129, 1, 1, 1, 300, 0, 64, 127, 2, 0], 8, 2, D, 3)
 
