@@ -72,14 +72,16 @@ constexpr int kMisses = 4096;  // claims in a row that brought no item
 constexpr uint32_t kTmemCols = 512;
 constexpr float kSlack = 8.0f;  // log2 of the growth of p that is let pass before m moves
 
-template <int D>
+// ONE: items of one tile.
+template <int D, bool ONE>
 struct Cfg {
     static constexpr int kCols = D / 64;               // 128-byte column blocks of a row
     static constexpr int kBlkBytes = kRows * 128;      // one column block of 128 rows
     static constexpr int kTileBytes = kCols * kBlkBytes;
     // columns of tensor memory: S of tile x at 128 x, O at 256 + D x, P over S, or (where O leaves room) behind O, so
-    // that S can be overwritten as soon as it is in registers
-    static constexpr bool kOwnP = D == 64;
+    // that S can be overwritten as soon as it is in registers (one prompt of 8,000 tokens, one head of 128: 81.8 us, with
+    // P over S 106.8)
+    static constexpr bool kOwnP = D == 64 || ONE;
     static constexpr uint32_t kPCol = kOwnP ? 384 : 0, kPStride = kOwnP ? 64 : 128;
     static constexpr int kStages = D == 128 ? 4 : 8;   // K and V blocks in the ring
     static constexpr int kRing = 2 * kTileBytes;       // after the two Q tiles
@@ -248,12 +250,12 @@ struct Wait {
 __device__ __forceinline__ uint32_t idesc_qk(int n) { return idesc_bf16_f32(kRows, n); }
 __host__ __device__ constexpr uint32_t idesc_pv(int d) { return idesc_bf16_f32(kRows, d) | (1u << 16); }
 
-template <int D>
+template <int D, bool ONE>
 __global__ void __launch_bounds__(kThreads, 1)
 prompt_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
                    const __grid_constant__ CUtensorMap vmap, const PromptArgs p)
 {
-    using C = Cfg<D>;
+    using C = Cfg<D, ONE>;
     constexpr uint32_t S = (uint32_t)C::kStages;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
@@ -740,8 +742,10 @@ int sms_of_device()
     if (sms == 0) {
         const cudaFuncAttribute limit = cudaFuncAttributeMaxDynamicSharedMemorySize;
         if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
-            cudaFuncSetAttribute(prompt_attn_kernel<64>, limit, Cfg<64>::kBytes + 1024) != cudaSuccess ||
-            cudaFuncSetAttribute(prompt_attn_kernel<128>, limit, Cfg<128>::kBytes + 1024) != cudaSuccess)
+            cudaFuncSetAttribute(prompt_attn_kernel<64, false>, limit, Cfg<64, false>::kBytes + 1024) != cudaSuccess ||
+            cudaFuncSetAttribute(prompt_attn_kernel<64, true>, limit, Cfg<64, true>::kBytes + 1024) != cudaSuccess ||
+            cudaFuncSetAttribute(prompt_attn_kernel<128, false>, limit, Cfg<128, false>::kBytes + 1024) != cudaSuccess ||
+            cudaFuncSetAttribute(prompt_attn_kernel<128, true>, limit, Cfg<128, true>::kBytes + 1024) != cudaSuccess)
             return 0;
         sms_of[dev].store(sms, std::memory_order_release);
     }
@@ -765,10 +769,11 @@ int run(const uint16_t *q, int64_t ldq, const uint16_t *k, int64_t ldk, const ui
     const int sms = sms_of_device();
     if (sms == 0) return -2;
     // Two tiles share a CTA's K and V and fill each other's waits; one to a CTA while that leaves SMs over (2,000 tokens, 4
-    // heads of 64: 23.0 us with one, 30.8 with two; 1,000 tokens, 16 / 2 heads of 128: 18.2 and 19.8)
+    // heads of 64: 23.2 us with one, 30.8 with two; 1,000 tokens, 16 / 2 heads of 128: 15.7 and 19.8)
     a.tiles = (a.M / a.tpt + a.B / 2) * a.H <= sms ? 1 : 2;
     const unsigned grid = (unsigned)items(a.M, a.B, a.tpt, a.H, a.tiles);
-    launch_behind(prompt_attn_kernel<D>, grid, kThreads, Cfg<D>::kBytes + 1024, st, qm, km, vm, a);
+    if (a.tiles == 1) launch_behind(prompt_attn_kernel<D, true>, grid, kThreads, Cfg<D, true>::kBytes + 1024, st, qm, km, vm, a);
+    else launch_behind(prompt_attn_kernel<D, false>, grid, kThreads, Cfg<D, false>::kBytes + 1024, st, qm, km, vm, a);
     return 0;
 }
 
