@@ -49,7 +49,7 @@
 // that fills the last round (M = 700, 8192 x 8192: 45.3 -> 38.9 us; M = 256,
 // 10240 x 8192: 27.9 -> 24.3).  Warp 0 of each CTA copies, its completions counted by
 // the leader CTA's barrier; in the leader, one thread of warp 1 issues the
-// pair's MMAs and their commits, which reach both CTAs; warps 2-5 turn one of
+// pair's MMAs and their commits, which reach both CTAs; warps 2-9 turn one of
 // two accumulators into bf16 while the MMAs fill the other.  Tiles are taken
 // round-robin in an order that walks the weight columns within a band of
 // activation rows small enough to stay in L2.  Measured: M = 8,190, N = 57,344,
@@ -71,10 +71,11 @@ constexpr int kRowBytes = 128;                // bytes of K per row and stage
 constexpr int kOperand = kHalf * kRowBytes;   // 16 KB
 constexpr int kStageBytes = 2 * kOperand;
 constexpr int kStages = 6;
-constexpr int kThreads = 192;
+constexpr int kOutWarps = 8;                  // epilogue warps: two per quarter of tensor memory, on alternate 32 columns
+constexpr int kThreads = 64 + 32 * kOutWarps;
 constexpr int kOutBytes = 32 * 64;            // per epilogue warp: 32 rows of 32 bf16
 constexpr int kOutOff = kStages * kStageBytes;
-constexpr int kScaleOff = kOutOff + 4 * kOutBytes;
+constexpr int kScaleOff = kOutOff + kOutWarps * kOutBytes;
 constexpr int kBarOff = kScaleOff + kTile * 4;
 constexpr int kSmem = kBarOff + 256;
 constexpr int64_t kBandBytes = 32 << 20;      // activation rows of a band: a quarter of L2
@@ -189,10 +190,10 @@ __device__ __forceinline__ void write_rows(const uint32_t v[32], float sx, const
             if (r < rows && 8 * piece < cols) *reinterpret_cast<uint4 *>(to + r * N + 8 * piece) = g;
         }
     } else {  // rows of y begin at any even address: one value per lane
-        for (int r = 0; r < rows; ++r) {
-            const int piece = (lane >> 3) ^ ((r >> 1) & 3);
-            const uint16_t h = *reinterpret_cast<const uint16_t *>(out + r * 64 + piece * 16 + (lane & 7) * 2);
-            if (lane < cols) to[r * N + lane] = h;
+#pragma unroll 8
+        for (int r = 0; r < 32; ++r) {
+            const uint16_t h = *reinterpret_cast<const uint16_t *>(out + r * 64 + ((lane >> 3) ^ ((r >> 1) & 3)) * 16 + (lane & 7) * 2);
+            if (r < rows && lane < cols) to[r * N + lane] = h;
         }
     }
     __syncwarp();
@@ -217,7 +218,7 @@ gemm_i8_pair_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_const
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&b.d_full[i], 1);
-            mbar_init(&b.d_empty[i], 8);  // 4 epilogue warps of each CTA
+            mbar_init(&b.d_empty[i], 2 * kOutWarps);  // the epilogue warps of both CTAs
         }
         mbar_init(&b.done, 1);
         b.abort = 0;
@@ -308,16 +309,16 @@ gemm_i8_pair_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_const
             int mi, ni;
             tile_at(p, t, mi, ni);
             const int64_t m0 = (int64_t)mi * kTile + rank * kHalf + quarter * 32, n0 = (int64_t)ni * 2 * p.each;
-            named_bar_sync(1, 128);  // the scales of the tile before have been read
-            for (int i = et; i < 2 * p.each; i += 128) sw[i] = n0 + i < p.N ? bf16_to_f32(p.ws[n0 + i]) : 0.0f;
-            named_bar_sync(1, 128);
+            named_bar_sync(1, 32 * kOutWarps);  // the scales of the tile before have been read
+            for (int i = et; i < 2 * p.each; i += 32 * kOutWarps) sw[i] = n0 + i < p.N ? bf16_to_f32(p.ws[n0 + i]) : 0.0f;
+            named_bar_sync(1, 32 * kOutWarps);
             const float sx = m0 + lane < p.M ? p.xs[m0 + lane] : 0.0f;
             const uint32_t buf = n & 1u;
             if (!wait(&b.d_full[buf], (n >> 1) & 1u)) break;
             tc_fence_after();
             const int rows = (int)min((int64_t)32, p.M - m0), cols = (int)min((int64_t)2 * p.each, p.N - n0);
 #pragma unroll 1
-            for (int c = 0; c < cols && rows > 0; c += 32) {
+            for (int c = (wid - 2) / 4 * 32; c < cols && rows > 0; c += 8 * kOutWarps) {
                 uint32_t v[32];
                 tmem_ld32(tmem + lane_bits + buf * 256u + (uint32_t)c, v);
                 tmem_wait_ld();
@@ -344,7 +345,7 @@ constexpr int kRowsStages = 24;               // at most
 constexpr int kRowsRing = 200 * 1024;
 constexpr int kLeastStages = 5;  // in the ring, before a stage takes more pieces of K
 constexpr int kRowsOut = kRowsRing + 8192;    // (the MMA reads 64 rows of tokens, stale ones behind the last stage's too)
-constexpr int kRowsScale = kRowsOut + 4 * kOutBytes;
+constexpr int kRowsScale = kRowsOut + kOutWarps * kOutBytes;
 constexpr int kRowsBar = kRowsScale + 256 * 4;
 constexpr int kRowsSmem = kRowsBar + 512;
 
@@ -385,7 +386,7 @@ gemm_i8_rows_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_const
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&b.d_full[i], 1);
-            mbar_init(&b.d_empty[i], 8);  // 4 epilogue warps of each CTA
+            mbar_init(&b.d_empty[i], 2 * kOutWarps);  // the epilogue warps of both CTAs
         }
         mbar_init(&b.done, 1);
         b.abort = 0;
@@ -481,17 +482,17 @@ gemm_i8_rows_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_const
             const int64_t first = 2 * (int64_t)(t / a.mt) * a.each, m0 = (int64_t)(2 * (t % a.mt) + (int)rank) * a.tokens + row;
             const int rows = (int)min((int64_t)min(32, a.tokens - row), p.M - m0);
             const float sx = lane < rows ? p.xs[m0 + lane] : 0.0f;
-            named_bar_sync(1, 128);  // the scales of the tile before have been read
-            for (int i = et; i < 2 * a.each; i += 128)
+            named_bar_sync(1, 32 * kOutWarps);  // the scales of the tile before have been read
+            for (int i = et; i < 2 * a.each; i += 32 * kOutWarps)
                 sw[i < a.each ? i : 128 + i - a.each] = first + i < p.N ? bf16_to_f32(p.ws[first + i]) : 0.0f;
-            named_bar_sync(1, 128);
+            named_bar_sync(1, 32 * kOutWarps);
             const uint32_t buf = n & 1u;
             if (!wait(&b.d_full[buf], (n >> 1) & 1u)) break;
             tc_fence_after();
             const int64_t n0 = first + half * a.each;
             const int cols = (int)min((int64_t)a.each, p.N - n0);
 #pragma unroll 1
-            for (int c = 0; c < cols && rows > 0; c += 32) {
+            for (int c = (wid - 2) / 4 * 32; c < cols && rows > 0; c += 8 * kOutWarps) {
                 uint32_t v[32];
                 tmem_ld32(tmem + lane_bits + buf * 128u + (uint32_t)c, v);
                 tmem_wait_ld();
@@ -533,6 +534,7 @@ struct Stream {
     static constexpr uint32_t kCols = 2 * BN;  // two accumulators
 };
 
+constexpr int kStreamThreads = 192;
 constexpr int kReader = 1 << 20;  // a counter's unit for CTAs that have read their share (the stages stay below it)
 constexpr int kColumns = 4;       // columns in flight per warp of the shared sum
 
@@ -575,7 +577,7 @@ struct StreamArgs {
 };
 
 template <int BN>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kStreamThreads)
 gemm_i8_stream_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CUtensorMap wmap, const StreamArgs p)
 {
     using C = Stream<BN>;
@@ -952,7 +954,7 @@ int run_stream(const int8_t *xq, const int8_t *wq, const Args &g, const Plan &pl
     if (plan.split > 1 && clear_extra_counters(workspace, plan.tiles, st) != cudaSuccess) return -2;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)a.plan.grid);
-    cfg.blockDim = dim3(kThreads);
+    cfg.blockDim = dim3(kStreamThreads);
     cfg.dynamicSmemBytes = C::kSmem + 1024;
     cfg.stream = st;
     cudaLaunchAttribute attr[2];
