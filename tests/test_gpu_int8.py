@@ -146,7 +146,7 @@ def test_matmul_shared_rows(M, N, K):
 
 
 # Tiles of 256 tokens by 160 to 256 weight rows on pairs of SMs, one to several rounds of them
-@pytest.mark.parametrize("M,N,K", [(700, 8191, 1056), (300, 57345, 160), (256, 10243, 512), (1500, 4099, 2080), (513, 14337, 288),
+@pytest.mark.parametrize("M,N,K", [(700, 8191, 1056), (300, 57345, 160), (1821, 17124, 128), (1000, 10242, 96), (100, 4100, 512), (256, 10243, 512), (1500, 4099, 2080), (513, 14337, 288),
                                    (2000, 20011, 96), (150, 40001, 1024), (129, 57344, 544), (4097, 1001, 2048)])
 def test_matmul_pair_tiles(M, N, K):
     check_matmul(M, N, K, M + N + K)
