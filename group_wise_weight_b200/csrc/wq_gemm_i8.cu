@@ -54,7 +54,7 @@
 // round-robin in an order that walks the weight columns within a band of
 // activation rows small enough to stay in L2.  Measured: M = 8,190, N = 57,344,
 // K = 8,192 in 2.27 ms, 3,390 TOPS with the tensor pipe 89% busy (2.69 ms
-// once the power cap lowers the clock); 2,048 x 8,192 x 8,192 94 us.
+// once the power cap lowers the clock); 2,048 x 8,192 x 8,192 86 us.
 #include <algorithm>
 #include <atomic>
 
