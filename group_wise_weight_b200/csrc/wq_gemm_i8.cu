@@ -9,7 +9,8 @@
 // Three kernels, all persistent, all fed by TMA with the 128-byte swizzle in
 // stages of 128 bytes of K (past K's end a copy fills in zeros, which add
 // nothing), accumulators double-buffered in tensor memory, every barrier wait
-// bounded (but a pair's two cluster barriers, which every thread reaches).
+// bounded (but a pair's two cluster barriers and the epilogue warps' named ones, which
+// every thread reaches whatever has run out).
 //
 // Few and middling rows (gemm_i8_rows_kernel): the weights bound the call, so
 // their rows are shared out evenly, rounded up to 8: up to 128 tokens N / 148 of
@@ -311,6 +312,7 @@ gemm_i8_pair_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_const
         const uint32_t d_empty[2] = {at_leader(&b.d_empty[0]), at_leader(&b.d_empty[1])};
         const int width = store_width(p.N);
         uint32_t n = 0;
+        bool ok = true;  // a warp whose wait has run out still meets the others at the barriers of the tiles that are left
         for (int t = pair; t < tiles; t += pairs, ++n) {
             int mi, ni;
             tile_at(p, t, mi, ni);
@@ -320,7 +322,8 @@ gemm_i8_pair_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_const
             named_bar_sync(1, 32 * kOutWarps);
             const float sx = m0 + lane < p.M ? p.xs[m0 + lane] : 0.0f;
             const uint32_t buf = n & 1u;
-            if (!wait(&b.d_full[buf], (n >> 1) & 1u)) break;
+            ok = ok && warp_wait(&b.d_full[buf], (n >> 1) & 1u, p.status, &b.abort);
+            if (!ok) continue;
             tc_fence_after();
             const int rows = (int)min((int64_t)32, p.M - m0), cols = (int)min((int64_t)2 * p.each, p.N - n0);
 #pragma unroll 1
@@ -484,6 +487,7 @@ gemm_i8_rows_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_const
         const int width = store_width(p.N);
         const int row = (quarter & 1) * 32;
         uint32_t n = 0;
+        bool ok = true;  // a warp whose wait has run out still meets the others at the barriers of the tiles that are left
         for (int t = pair; t < a.tiles; t += pairs, ++n) {
             const int64_t first = 2 * (int64_t)(t / a.mt) * a.each, m0 = (int64_t)(2 * (t % a.mt) + (int)rank) * a.tokens + row;
             const int rows = (int)min((int64_t)min(32, a.tokens - row), p.M - m0);
@@ -493,7 +497,8 @@ gemm_i8_rows_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_const
                 sw[i < a.each ? i : 128 + i - a.each] = first + i < p.N ? bf16_to_f32(p.ws[first + i]) : 0.0f;
             named_bar_sync(1, 32 * kOutWarps);
             const uint32_t buf = n & 1u;
-            if (!wait(&b.d_full[buf], (n >> 1) & 1u)) break;
+            ok = ok && warp_wait(&b.d_full[buf], (n >> 1) & 1u, p.status, &b.abort);
+            if (!ok) continue;
             tc_fence_after();
             const int64_t n0 = first + half * a.each;
             const int cols = (int)min((int64_t)a.each, p.N - n0);
@@ -682,10 +687,11 @@ gemm_i8_stream_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_con
         const int64_t M = p.g.M, N = p.g.N;
         uint32_t n = 0;
         int64_t sx_at = -1;
-        bool ok = true;
-        for (int64_t u = beg; u < end; ++n) {
+        bool ok = true;  // a warp whose wait has run out still meets the others at the barriers that are left
+        for (int64_t u = beg, next; u < end; u = next, ++n) {
             const int64_t tile = u / stages;
             const int s0 = (int)(u - tile * stages), s1 = (int)std::min<int64_t>(stages, s0 + (end - u));
+            next = u + (s1 - s0);
             const int64_t nr = tile % nt * 128 + r, m0 = tile / nt * BN;
             const int cols = (int)std::min<int64_t>(BN, M - m0);
             const float sw = nr < N ? bf16_to_f32(p.g.ws[nr]) : 0.0f;
@@ -695,13 +701,13 @@ gemm_i8_stream_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_con
                 named_bar_sync(1, 128);
                 sx_at = m0;
             }
-            if (!wait(&b.d_full[n & 1u], (n >> 1) & 1u)) { ok = false; break; }
+            ok = ok && warp_wait(&b.d_full[n & 1u], (n >> 1) & 1u, p.g.status, &b.abort);
             tc_fence_after();
             const uint32_t d = tmem + lane_bits + (n & 1u) * (uint32_t)BN;
             if (count > 1) {  // the sums to the tile's parts: [part][column][row]
                 int *part = p.part + (tile * count + mine) * (BN * 128) + r;
 #pragma unroll 1
-                for (int c = 0; c < cols; c += 16) {
+                for (int c = 0; c < cols && ok; c += 16) {
                     uint32_t v[16];
                     tmem_ld16(d + (uint32_t)c, v);
                     tmem_wait_ld();
@@ -710,9 +716,9 @@ gemm_i8_stream_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_con
                         if (c + e < cols) part[(c + e) * 128] = (int)v[e];
                 }
                 __threadfence();
-                named_bar_sync(1, 128);
-                if (tid == 64) atomicAdd(p.counters + tile, s1 - s0);
-            } else {
+                ok = named_bar_and(1, 128, ok);  // one answer for the four warps, which join the tile's sums together
+                if (ok && tid == 64) atomicAdd(p.counters + tile, s1 - s0);
+            } else if (ok) {
 #pragma unroll 1
                 for (int c = 0; c < cols; c += 16) {
                     uint32_t v[16];
@@ -728,10 +734,10 @@ gemm_i8_stream_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_con
                     }
                 }
             }
+            if (!ok) continue;
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&b.d_empty[n & 1u]);
-            u += s1 - s0;
         }
         if (count > 1 && ok) {
             // this CTA's share of its tile's columns

@@ -27,6 +27,24 @@ __device__ __forceinline__ uint32_t pack2_bf16(float a, float b)
     return r;
 }
 
+// mbar_wait by a whole warp, with one answer for all lanes: what follows a wait (tensor-memory loads, votes, barriers) needs
+// every lane, and lanes that gave up one by one would leave the others waiting for them without a bound.
+__device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, int *status, volatile int *abort)
+{
+    return __all_sync(0xffffffffu, mbar_wait(bar, parity, status, abort));
+}
+
+// named_bar_sync whose threads learn whether `ok` held for all of them.
+__device__ __forceinline__ bool named_bar_and(int id, int threads, bool ok)
+{
+    uint32_t all;
+    asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.u32 q, %3, 0;\n\tbar.red.and.pred p, %1, %2, q;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+                 : "=r"(all)
+                 : "r"(id), "r"(threads), "r"((uint32_t)ok)
+                 : "memory");
+    return all != 0;
+}
+
 // One lane of the (whole) warp.
 __device__ __forceinline__ bool elect_one()
 {
