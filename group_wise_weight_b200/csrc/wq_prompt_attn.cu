@@ -237,12 +237,22 @@ __device__ __forceinline__ void drain(uint64_t *bar, uint32_t parity, int *statu
         if (global_ns() - since > kWaitLimitNs) { record_timeout(status); return; }
 }
 
+// For one thread, and for a whole warp (one answer for all its lanes).
 struct Wait {
     int *status;
     volatile int *abort;
     __device__ __forceinline__ bool operator()(uint64_t *bar, uint32_t parity) const
     {
         return mbar_wait(bar, parity, status, abort);
+    }
+};
+
+struct WarpWait {
+    int *status;
+    volatile int *abort;
+    __device__ __forceinline__ bool operator()(uint64_t *bar, uint32_t parity) const
+    {
+        return warp_wait(bar, parity, status, abort);
     }
 };
 
@@ -261,7 +271,7 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_consta
     uint8_t *smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
     Bars &b = *reinterpret_cast<Bars *>(smem + C::kBarOff);
     const int tid = threadIdx.x, wid = tid >> 5, lane = tid & 31;
-    const Wait wait{p.status, &b.abort};
+    const WarpWait wait{p.status, &b.abort};
 
     if (tid == 0) {
         for (uint32_t i = 0; i < S; ++i) {
@@ -365,6 +375,7 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_consta
         // ------------------------------ MMAs: one thread ------------------------------
         registers_dec<kOtherRegs>();
         if (elect_one()) {
+            const Wait wait{p.status, &b.abort};
             uint32_t slot = 0, phase = 0, nitem = 0;
             struct Tile {
                 uint32_t sn, pn, qn, on;  // S and P V issued, items begun by S and by P V

@@ -108,3 +108,24 @@ def test_epilogue_lanes_get_one_answer(kernel):
     assert "warp_wait(" in body
     helper = source("wq_prompt.cuh")
     assert "__all_sync(0xffffffffu, mbar_wait(" in block(helper, helper.index("bool warp_wait("))
+
+
+@pytest.mark.parametrize("marker", ["items and copies", "softmax, one row per thread", "output, both tiles in turn", "Q of tile x"])
+def test_attention_roles_of_whole_warps_get_one_answer(marker):
+    """Votes, shuffles and tensor-memory loads follow the waits of these roles."""
+    text = source("wq_prompt_attn.cu")
+    body = block(text, text.index(")\n{", text.index("prompt_attn_kernel(const __grid_constant__")))
+    kind = re.search(r"const (\w+) wait\{", body).group(1)  # the kernel's; a role may have its own
+    own = role("prompt_attn_kernel", marker)
+    kind = m.group(1) if (m := re.search(r"const (\w+) wait\{", own)) else kind
+    assert "wait(" in own and "mbar_wait(" not in own
+    assert "return warp_wait(bar, parity, status, abort);" in block(text, text.index(f"struct {kind} "))
+
+
+def test_attention_role_of_one_thread_votes_with_nobody():
+    own = role("prompt_attn_kernel", "MMAs: one thread")
+    at = own.index("if (elect_one())")
+    kind = re.search(r"const (\w+) wait\{", block(own, at)).group(1)
+    text = source("wq_prompt_attn.cu")
+    assert "return mbar_wait(bar, parity, status, abort);" in block(text, text.index(f"struct {kind} "))
+    assert "wait(" not in own[:at]
