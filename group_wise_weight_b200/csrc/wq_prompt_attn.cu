@@ -563,7 +563,9 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_consta
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&b.s_free[x]);
-                    return blocks_done == 0 || wait(&b.pv_done[x], (blocks_done - 1) & 1u);
+                    if (blocks_done > 0 && !wait(&b.pv_done[x], (blocks_done - 1) & 1u)) return false;
+                    tc_fence_after();  // what follows touches O and P, which that product wrote and read
+                    return true;
                 };
                 if (u0 + kKeys <= tile_tok + 1) {  // every row sees every key of the block
                     uint32_t v[kKeys / 32][32];

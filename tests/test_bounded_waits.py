@@ -129,3 +129,21 @@ def test_attention_role_of_one_thread_votes_with_nobody():
     text = source("wq_prompt_attn.cu")
     assert "return mbar_wait(bar, parity, status, abort);" in block(text, text.index(f"struct {kind} "))
     assert "wait(" not in own[:at]
+
+
+def test_attention_fences_after_every_wait_for_an_mma():
+    """tcgen05 loads and stores are ordered behind an MMA's completion by a fence after the wait for it, not by the wait
+    alone: in the softmax and output roles each wait on a barrier that a commit arrives on is followed by one before
+    any tensor-memory access."""
+    text = source("wq_prompt_attn.cu")
+    committed = set(re.findall(r"tc_commit\(&b\.(\w+)", text))
+    assert {"s_full", "pv_done"} <= committed
+    access = re.compile(r"tmem_(?:ld|st)\d+\(|tc_fence_after\(\)")
+    for marker in ("softmax, one row per thread", "output, both tiles in turn"):
+        own = role("prompt_attn_kernel", marker)
+        waits = [m for m in re.finditer(r"wait\(&b\.(\w+)", own) if m.group(1) in committed]
+        assert waits
+        for m in waits:
+            # the function that holds a wait at its end returns to a caller that touches tensor memory next
+            follows = access.search(own, m.end())
+            assert follows and follows.group().startswith("tc_fence_after"), own[m.start():m.start() + 200]
