@@ -516,12 +516,14 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_consta
                 if (!wait(&b.s_full[x], blocks_done & 1u)) { ok = false; break; }
                 tc_fence_after();
                 const int u0 = j * kKeys, keys = min(kKeys, last - u0);
-                // m follows the block's maximum `top` of the row once p would grow by more than 2^kSlack
+                // m follows the block's maximum `top` of the row once p would grow by more than 2^kSlack.  The vote only skips
+                // the pass over O: which m a row carries is its own affair, or the rows around it (later tokens, the next
+                // sequence's, what shared memory held) would decide how its p is rounded.
                 auto move_max = [&](float top) {
                     const bool grow = (top - m) * p.scale_log2 > kSlack;
                     if (!__any_sync(0xffffffffu, grow)) return;
-                    const float keep = ex2((m - top) * p.scale_log2);
-                    m = top;
+                    const float keep = grow ? ex2((m - top) * p.scale_log2) : 1.0f;
+                    m = grow ? top : m;
                     l *= keep;
                     if (j == 0) return;
                     // the product of the block before has completed: S was issued after it, or it was waited for
