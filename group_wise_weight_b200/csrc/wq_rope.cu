@@ -103,10 +103,11 @@ __device__ __forceinline__ void load_heads(Batch &x, const uint16_t *src, int ba
     }
 }
 
-// Turns them, `first` and the lane's weights w1, w2 being loaded already.
+// Turns them (or lets them pass, where the lane is not `turned`), `first` and the lane's weights w1, w2 being loaded already.
 template <int D, bool INTERLEAVED, bool NORM>
 __device__ __forceinline__ void turn_heads(Batch &first, const uint16_t *src, uint16_t *dst, int base, int g, int step, int heads,
-                                           int o1, int o2, uint2 w1, uint2 w2, const float c[4], const float s[4], float eps)
+                                           int o1, int o2, uint2 w1, uint2 w2, const float c[4], const float s[4], bool turned,
+                                           float eps)
 {
     constexpr int L = D / 8;  // lanes per head
     float wa[4], wb[4];
@@ -147,8 +148,12 @@ __device__ __forceinline__ void turn_heads(Batch &first, const uint16_t *src, ui
             }
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                ya[i] = fma2_pairs(x.b[i], bs[i], mul2(x.a[i], ac[i]));
-                yb[i] = fma2_pairs(x.a[i], as[i], mul2(x.b[i], bc[i]));
+                ya[i] = mul2(x.a[i], ac[i]);
+                yb[i] = mul2(x.b[i], bc[i]);
+                if (turned) {  // values that pass meet no other (an infinity times sin 0 would be NaN, -0 + 0 lose its sign)
+                    ya[i] = fma2_pairs(x.b[i], bs[i], ya[i]);
+                    yb[i] = fma2_pairs(x.a[i], as[i], yb[i]);
+                }
                 if (NORM) {
                     ya[i] = mul2(ya[i], f32x2{inv, inv});
                     yb[i] = mul2(yb[i], f32x2{inv, inv});
@@ -215,7 +220,7 @@ qk_norm_rope_kernel(const RopeArgs p)
         s[0] = sv.x; s[1] = sv.y; s[2] = sv.z; s[3] = sv.w;
     }
     uint16_t *dst = keys ? p.ko + m * p.ldko : p.qo + m * p.ldqo;
-    turn_heads<D, INTERLEAVED, NORM>(first, src, dst, base, g, step, heads, o1, o2, w1, w2, c, s, p.eps);
+    turn_heads<D, INTERLEAVED, NORM>(first, src, dst, base, g, step, heads, o1, o2, w1, w2, c, s, turned, p.eps);
     if (p.split > 1) return;
     src = p.k + m * p.ldk;
     load_heads<D, INTERLEAVED>(first, src, 0, g, kHeads, p.H, o1, o2);
@@ -223,7 +228,7 @@ qk_norm_rope_kernel(const RopeArgs p)
         w1 = *reinterpret_cast<const uint2 *>(p.kw + o1);
         w2 = *reinterpret_cast<const uint2 *>(p.kw + o2);
     }
-    turn_heads<D, INTERLEAVED, NORM>(first, src, p.ko + m * p.ldko, 0, g, kHeads, p.H, o1, o2, w1, w2, c, s, p.eps);
+    turn_heads<D, INTERLEAVED, NORM>(first, src, p.ko + m * p.ldko, 0, g, kHeads, p.H, o1, o2, w1, w2, c, s, turned, p.eps);
 }
 
 template <int D, bool INTERLEAVED>
