@@ -6,7 +6,9 @@ quantisers rely on IEEE division and round-to-nearest-even), then linked
 into group_wise_weight_b200/libwq.so.  The binding of the prompt-side calls
 (csrc/wq_torch.cpp, a CPython extension on torch's headers) is compiled with
 g++ into group_wise_weight_b200/_wq_torch.so and linked against libwq.so
-beside it.  Objects are rebuilt only when a source or header is newer.
+beside it.  Objects are rebuilt only when a source or header is newer; the
+binding also when the torch or Python that it was compiled against differs
+from the present one (recorded in _build/ beside the objects).
 """
 from __future__ import annotations
 
@@ -15,6 +17,7 @@ import glob
 import os
 import shutil
 import subprocess
+import sys
 import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -23,6 +26,7 @@ CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libwq.so")
 BINDING = os.path.join(PKG, "_wq_torch.so")
+BINDING_STAMP = os.path.join(BUILD, "wq_torch.stamp")
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",
@@ -46,6 +50,25 @@ def _stale(target: str, inputs) -> bool:
         return True
     t = os.path.getmtime(target)
     return any(os.path.getmtime(p) > t for p in inputs)
+
+
+def _binding_stamp() -> str:
+    """What a compiled binding is bound to: torch's C++ classes, Python's ABI, and how it was compiled (no paths of this
+    checkout, which may move)."""
+    import torch
+
+    return "\n".join([f"torch {torch.__version__} {torch.version.git_version} cuda {torch.version.cuda}",
+                      f"cxx11abi {int(torch.compiled_with_cxx11_abi())}",
+                      f"python {sys.version} {sysconfig.get_config_var('SOABI')}"]
+                     + [a for a in _binding_command("") if not os.path.isabs(a.removeprefix("-I").removeprefix("-L"))])
+
+
+def _read(path: str):
+    try:
+        with open(path) as f:
+            return f.read()
+    except OSError:
+        return None
 
 
 def _binding_command(src: str):
@@ -89,12 +112,15 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
         run(cmd)
         os.replace(LIB + ".tmp", LIB)
     binding_src = os.path.join(CSRC, "wq_torch.cpp")
-    if force or _stale(BINDING, [binding_src] + glob.glob(os.path.join(ROOT, "include", "*.h"))):
+    stamp = _binding_stamp()
+    if (force or _stale(BINDING, [binding_src] + glob.glob(os.path.join(ROOT, "include", "*.h")))
+            or _read(BINDING_STAMP) != stamp):
         run(_binding_command(binding_src))
         os.replace(BINDING + ".tmp", BINDING)
+        with open(BINDING_STAMP, "w") as f:
+            f.write(stamp)
     return LIB
 
 
 if __name__ == "__main__":
-    import sys
     print(build(force="--force" in sys.argv, verbose=True, ptxas_info="--ptxas" in sys.argv))
