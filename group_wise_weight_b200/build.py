@@ -8,7 +8,10 @@ into group_wise_weight_b200/libwq.so.  The binding of the prompt-side calls
 g++ into group_wise_weight_b200/_wq_torch.so and linked against libwq.so
 beside it.  Objects are rebuilt only when a source or header is newer; the
 binding also when the torch or Python that it was compiled against differs
-from the present one (recorded in _build/ beside the objects).
+from the present one (recorded in _build/ beside the objects).  Where g++ or
+the headers of Python or torch are missing the binding is left out with a
+warning: libwq.so and every call that goes through it alone need none of
+them, and the prompt-side calls raise.
 """
 from __future__ import annotations
 
@@ -19,6 +22,7 @@ import shutil
 import subprocess
 import sys
 import sysconfig
+import warnings
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -71,10 +75,23 @@ def _read(path: str):
         return None
 
 
+def _torch_home() -> str:
+    import torch
+
+    return os.path.dirname(torch.__file__)
+
+
+def _binding_lacks():
+    """What the binding cannot be compiled without and this machine does not have."""
+    headers = [os.path.join(sysconfig.get_paths()["include"], "Python.h"),
+               os.path.join(_torch_home(), "include", "torch", "csrc", "autograd", "python_variable.h")]
+    return [h for h in headers if not os.path.exists(h)] + ([] if shutil.which("g++") else ["g++"])
+
+
 def _binding_command(src: str):
     import torch
 
-    home = os.path.dirname(torch.__file__)
+    home = _torch_home()
     cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
     inc = [os.path.join(home, "include"), os.path.join(home, "include", "torch", "csrc", "api", "include"),
            os.path.join(cuda, "include"), sysconfig.get_paths()["include"]]
@@ -99,7 +116,7 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
     def run(cmd):
         r = subprocess.run(cmd, capture_output=True, text=True)
         if r.returncode != 0:
-            raise RuntimeError("nvcc failed:\n" + " ".join(cmd) + "\n" + r.stdout + r.stderr)
+            raise RuntimeError(f"{os.path.basename(cmd[0])} failed:\n" + " ".join(cmd) + "\n" + r.stdout + r.stderr)
         return r.stdout + r.stderr
 
     if jobs:
@@ -115,6 +132,13 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
     stamp = _binding_stamp()
     if (force or _stale(BINDING, [binding_src] + glob.glob(os.path.join(ROOT, "include", "*.h")))
             or _read(BINDING_STAMP) != stamp):
+        lacks = _binding_lacks()
+        if lacks:
+            if os.path.exists(BINDING):  # it belongs to other sources or another torch or Python
+                os.remove(BINDING)
+            warnings.warn(f"{os.path.basename(BINDING)}, the binding of the prompt-side calls, is left out: "
+                          f"{', '.join(lacks)} not found")
+            return LIB
         run(_binding_command(binding_src))
         os.replace(BINDING + ".tmp", BINDING)
         with open(BINDING_STAMP, "w") as f:

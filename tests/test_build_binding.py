@@ -54,3 +54,35 @@ def test_a_newer_source_compiles_the_binding_again(commands):
     os.utime(wqbuild.BINDING, (0, 0))
     wqbuild.build()
     assert [c[0] for c in commands] == ["g++"]
+
+
+def test_without_headers_the_library_is_built_all_the_same(commands, monkeypatch, tmp_path):
+    """libwq.so serves the calls that do not go through the binding; those that do say what is missing."""
+    os.utime(wqbuild.BINDING, (0, 0))
+    paths = wqbuild.sysconfig.get_paths()
+    monkeypatch.setattr(wqbuild.sysconfig, "get_paths", lambda: {**paths, "include": str(tmp_path)})
+    with pytest.warns(UserWarning, match="Python.h"):
+        assert wqbuild.build() == wqbuild.LIB
+    assert commands == [] and not os.path.exists(wqbuild.BINDING)
+    import group_wise_weight_b200 as wq
+    monkeypatch.setattr(wq, "_native_module", None)
+    monkeypatch.setattr(wq, "BINDING_PATH", wqbuild.BINDING)
+    wq.lib()
+    with pytest.raises(RuntimeError, match="_wq_torch.so not found"):
+        wq.wq_quantize_int8_tokens(torch.zeros(4, 256))
+
+
+def test_without_a_compiler_the_library_is_built_all_the_same(commands, monkeypatch):
+    os.utime(wqbuild.BINDING, (0, 0))
+    known = shutil.which
+    monkeypatch.setattr(wqbuild.shutil, "which", lambda n: None if n == "g++" else known(n))
+    with pytest.warns(UserWarning, match="g\\+\\+ not found"):
+        assert wqbuild.build() == wqbuild.LIB
+    assert commands == []
+
+
+def test_a_binding_that_does_not_compile_fails_the_build(commands, monkeypatch):
+    os.utime(wqbuild.BINDING, (0, 0))
+    monkeypatch.setattr(wqbuild.subprocess, "run", lambda cmd, **kw: subprocess.CompletedProcess(cmd, 1, "", "error: x"))
+    with pytest.raises(RuntimeError, match="error: x"):
+        wqbuild.build()
