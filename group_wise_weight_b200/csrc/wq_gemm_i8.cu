@@ -54,8 +54,8 @@
 // two accumulators into bf16 while the MMAs fill the other.  Tiles are taken
 // round-robin in an order that walks the weight columns within a band of
 // activation rows small enough to stay in L2.  Measured: M = 8,190, N = 57,344,
-// K = 8,192 in 2.27 ms, 3,390 TOPS with the tensor pipe 89% busy (2.69 ms
-// once the power cap lowers the clock); 2,048 x 8,192 x 8,192 86 us.
+// K = 8,192 in 2.23 to 2.26 ms, 3,410 to 3,457 TOPS with the tensor pipe 89% busy
+// (2.49 to 2.65 ms once the power cap lowers the clock); 2,048 x 8,192 x 8,192 86 us.
 #include <algorithm>
 #include <atomic>
 
@@ -891,8 +891,9 @@ PairPlan plan_pairs(int64_t M, int64_t N, int sms)
 //   stream, whole tiles: a CTA takes ceil(tiles / SMs) of them; a stage takes 0.25 where few CTAs run, and what HBM gives
 //     it with every SM at work; a token's stores 0.025
 //   stream, split: the same number of CTAs for every tile, 8 stages at least to each, and the adding up
-// Fitted to and checked against 250 shapes of 1 to 2000 tokens, where what it takes is within 5% of the best but for
-// 17 (within 14%).  Measured, taken (not taken): M = 16, 8192 x 8192: rows 14.7 (split 17.1); M = 100, 57344 x 8192: rows 82
+// The rows' and pairs' stores are not in it, which decide where K is small (1821 x 17124 x 128: 33.6 us, its bytes 9.9): there
+// it compares main loops only.  Fitted to 250 shapes of 1 to 2000 tokens; over the same shapes what it takes is within 5%
+// of the best but for 17 (within 14%).  No others were held back to check it.  Measured, taken (not taken): M = 16, 8192 x 8192: rows 14.7 (split 17.1); M = 100, 57344 x 8192: rows 82
 // (whole 89); M = 128, 2048 x 8192: rows 8.7 (split 13.7); M = 256, 8192 x 8192: rows 19.0 (whole 22.7); M = 512, the same:
 // pairs 26.9 (rows 31.7); M = 1, 14336 x 4096: whole 11.9 (rows 13.2); M = 1, 1000 x 28672: split 15.3 (rows 18.4).
 constexpr double kUnit = 0.25, kUnitAll = 0.36, kPair = 0.33;

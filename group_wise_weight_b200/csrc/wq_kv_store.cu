@@ -22,8 +22,9 @@
 // (wq_quotient.cuh): one correction step for the bf16 scales of int4, two for
 // the arbitrary binary32 scale of fp8; blocks outside the proven range use
 // the IEEE division.
-// Measured, 16,000 tokens of 8 heads: fp8 18.8 us (5.2 TB/s; 20.6 without the
-// launch while the previous kernel ends), int4 25 us (3.3 TB/s); the schedulers issue 70% of the time, so the instructions bind.  The
+// Measured, 16,000 tokens of 8 heads, back to back: fp8 19.2 us (5.1 TB/s; 20.6
+// without the launch while the previous kernel ends), int4 23.1 us (3.6 TB/s);
+// the schedulers issue 69 and 75% of the time, so the instructions bind.  The
 // blocks of a lane are left to other warps (one vector per group of lanes):
 // several in turn per warp took 22.8 us.
 #include <algorithm>

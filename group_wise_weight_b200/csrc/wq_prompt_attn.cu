@@ -13,7 +13,8 @@
 // are scaled by e^(m_old - m_new).  Scaling is put off until m would grow by
 // more than a factor of 2^8 in p (p, l and the accumulator then carry the old
 // m, exactly; binary32 has room for 2^8 L), which leaves it to the first few
-// blocks of most rows.  Scores, m, l and the accumulator are binary32; p is
+// blocks of most rows; putting it off is a published refinement of that method
+// too.  Each row decides by its own scores.  Scores, m, l and the accumulator are binary32; p is
 // rounded to bf16 as the second product's operand (at most 2^-8 of each
 // term), while l sums the unrounded p.
 //
@@ -35,10 +36,11 @@
 // of the tensor core per tile and its 16,384 exponentials as many of the
 // special-function units, so both are at their limits together (heads of 64:
 // half the products, the exponentials alone).  Measured, causal halves only:
-// one sequence of 16,384 tokens, 64 query and 8 KV heads of 128, 3.34 ms
-// (1,317 TFLOP/s; 3.94 ms once the power cap lowers the clock); 32 query heads
-// of 64, 1.35 ms (817).  Short prompts lose the ends: 48 of 1 to 331 tokens,
-// 64 query heads, 76 us.  A block of 64 keys with two S tiles, a polynomial for
+// one sequence of 16,384 tokens, 64 query and 8 KV heads of 128, 3.32 to 3.43 ms
+// (1,282 to 1,325 TFLOP/s; 3.96 ms once the power cap lowers the clock); 32 query
+// heads of 64, 1.35 ms (812).  Short prompts lose the ends: 48 of 1 to 331 tokens,
+// 64 query heads, 78 us (76 with waits answered lane by lane and a warp's rows
+// moving m together, which is wrong: see warp_wait and move_max).  A block of 64 keys with two S tiles, a polynomial for
 // part of the exponentials, softmax warpgroups that take turns and key blocks
 // asked into L2 ahead each gained nothing.
 //
@@ -51,7 +53,7 @@
 // Keys past a tile's last visible one are left out of both products in steps
 // of 16; inside the step their p is 0, and the copy warp zeroes the V rows past
 // the sequence's end, so what lies behind a sequence never enters a sum.
-// Every barrier wait is bounded.
+// Every barrier wait is bounded, with one answer for a warp that waits as a whole.
 #include <algorithm>
 #include <atomic>
 

@@ -26,8 +26,8 @@
 // queries and keys apart.  The first heads' loads are under way while the
 // sines and cosines are formed, and the kernel starts while the previous one
 // ends (without the two 128 tokens took 7.3 us, 16,384 104).
-// Measured: 16,384 tokens, 64 + 8 heads of 128 with norms, 100 us (6.0 TB/s,
-// 92% of a copy); 128 tokens 5.0 us, 3.7 in a graph: launch and load latency.
+// Measured: 16,384 tokens, 64 + 8 heads of 128 with norms, 102 us (5.9 TB/s,
+// 90% of a copy); 128 tokens 5.1 us, 3.7 in a graph: launch and load latency.
 #include <algorithm>
 
 #include "wq_internal.h"

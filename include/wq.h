@@ -536,7 +536,7 @@ int wq_gemm_w8a8_int8(const int8_t *xq, const float *xscales, int64_t M, int64_t
  *   n_i = x_i / sqrt(mean(x^2) + eps) * w_i      (x itself when both weights are NULL)
  *   pairs (a, b) of the first `rot` values turn by the angle positions[m] * inv_freq[i]:
  *     (a cos - b sin, b cos + a sin); pair i is (i, i + rot/2), or (2i, 2i + 1)
- *     when `interleaved` is not 0; values rot .. D - 1 are not turned.
+ *     when `interleaved` is not 0; values rot .. D - 1 are not turned (without weights they keep their bits).
  * Sums, norms and rotations are binary32 (the angle is formed and reduced in
  * binary64), rounded to bf16 once.
  *
@@ -600,7 +600,9 @@ int wq_kv_store_fp8(const uint16_t *k, int64_t ldk, const uint16_t *v, int64_t l
  *             (infinities and NaN too), changes nothing
  * Scores, the running maximum and sum and the accumulator are binary32; p
  * is rounded to bf16 as the second product's operand, o once.  Repeated calls
- * give identical bytes.  Within a sequence, an infinity or NaN in k or v at
+ * give identical bytes, and a token's output depends to the bit on nothing but
+ * its own query and the (finite) keys and values it sees, given M, B and the
+ * bounds of the sequences.  Within a sequence, an infinity or NaN in k or v at
  * token u leaves o unspecified from 127 tokens before u on (a product over 16
  * keys multiplies v by the zeros of unseen keys), in q at its own token.
  * Requirements: B, M >= 1; D 64 or 128, Hq % H == 0, Hq / H <= 64
