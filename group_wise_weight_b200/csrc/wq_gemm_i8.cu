@@ -55,7 +55,7 @@
 // round-robin in an order that walks the weight columns within a band of
 // activation rows small enough to stay in L2.  Measured: M = 8,190, N = 57,344,
 // K = 8,192 in 2.23 to 2.26 ms, 3,410 to 3,457 TOPS with the tensor pipe 89% busy
-// (2.49 to 2.65 ms once the power cap lowers the clock); 2,048 x 8,192 x 8,192 86 us.
+// (2.49 to 2.76 ms once the power cap lowers the clock); 2,048 x 8,192 x 8,192 86 us.
 #include <algorithm>
 #include <atomic>
 
